@@ -417,6 +417,75 @@ int fgmm_ivf_search(int K, int D, const float* centroids, const int64_t* offsets
                     int64_t nq, int64_t ldq, int nprobe, int topk, int64_t* out_ids,
                     float* out_dist, int64_t* dco_out, fgmm_stream_t stream);
 
+/* 4-bit codes of vectors (OCP Microscaling Formats v1.0, MXFP4): every row of X in blocks of
+ * 32 values, each block one power-of-two scale (e8m0: byte s stands for 2^(s - 127), 255 for
+ * NaN) and 32 codes (e2m1: sign, magnitudes 0 0.5 1 1.5 2 3 4 6).  Stateless, device pointers,
+ * asynchronous on `stream` of the current device.
+ *
+ * Encoding of a block with largest magnitude a: s - 127 = floor(log2 a) - 2, at least -127; the
+ * codes are x / 2^(s - 127) rounded to the nearest magnitude (ties to the even code, above 6 to
+ * 6).  A block of zeros has s = 0.  A block that holds a NaN or an infinity has s = 255 and
+ * decodes to 32 NaNs.
+ *
+ * codes: [N][ceil(D / 32) * 16] bytes, two codes a byte, the lower dimension in the low nibble;
+ * the last block is padded with zeros.  scales: tiles of 128 rows x 4 blocks, 512 bytes each,
+ * [ceil(N / 128)][ceil(ceil(D / 32) / 4)][512], row r and block b of a tile at byte
+ * (r % 32) * 16 + (r / 32) * 4 + b (the order in which the tensor cores take them); the padding
+ * is 0.  Both are 16-byte aligned and caller-owned.  1 <= D, 0 <= N (N = 0 does nothing);
+ * N <= FGMM_MX4_MAX_ROWS and D <= FGMM_MX4_MAX_D (FGMM_ERR_UNSUPPORTED above).
+ *
+ * fgmm_mx4_encode: X row-major [N, D], row stride ldx, x_dtype FGMM_F32 or FGMM_BF16, any
+ * alignment of its elements' own size.
+ *
+ * fgmm_mx4_decode: the values that the codes stand for, exactly, as FGMM_F32 or FGMM_BF16 rows
+ * of stride ldo.
+ *
+ * fgmm_mx4_scores: out[m][n] = alpha * sum_d q[m][d] x[n][d] + bias[n] for codes of M queries and
+ * of N vectors of the same D (the padding adds 0); bias: optional device float[N] (-|x|^2 / 2
+ * ranks by L2 distance).  Products and sums are fp32; out_dtype FGMM_F32 or FGMM_BF16, rows of
+ * stride ldo >= N.  status: optional device int, set to FGMM_ERR_TIMEOUT if a bounded wait of the
+ * kernel expires (the output is then undefined), else left as it is. */
+#define FGMM_MX4_MAX_ROWS ((1ll << 31) - 1024)
+#define FGMM_MX4_MAX_D (1 << 20)
+size_t fgmm_mx4_codes_bytes(int64_t N, int D);
+size_t fgmm_mx4_scales_bytes(int64_t N, int D);
+int fgmm_mx4_encode(const void* X, int x_dtype, int64_t N, int D, int64_t ldx, uint8_t* codes,
+                    uint8_t* scales, fgmm_stream_t stream);
+int fgmm_mx4_decode(const uint8_t* codes, const uint8_t* scales, int64_t N, int D, void* out,
+                    int out_dtype, int64_t ldo, fgmm_stream_t stream);
+int fgmm_mx4_scores(const uint8_t* q_codes, const uint8_t* q_scales, int64_t M,
+                    const uint8_t* codes, const uint8_t* scales, int64_t N, int D, float alpha,
+                    const float* bias, void* out, int out_dtype, int64_t ldo, int* status,
+                    fgmm_stream_t stream);
+
+/* One draw per row of scores from its truncated softmax, with given uniforms (the method's
+ * randomness is an input, as in fgmm_kmeans_seed).  Stateless, device pointers, asynchronous.
+ *
+ * Row l[0 .. V-1] (logits, row stride ld; -inf forbids a token), weights
+ * w_i = exp((l_i - max l) / temperature).  Tokens are ordered by l, ties to the lower index, and
+ * truncated in three steps: the first top_k; of these the shortest prefix that holds top_p of
+ * their weight (a token stays when the weight before it is below top_p times the whole; the first
+ * always stays); of these the tokens with w_i >= min_p.  The draw is the smallest index i at which
+ * the running weight of the kept tokens, in index order, exceeds u times their whole weight.
+ *   temperature : float[rows], >= 0 and finite; 0 takes the first maximum; NULL: 1
+ *   top_k       : int32[rows]; <= 0 or >= V keeps all; NULL: all
+ *   top_p       : float[rows], in (0, 1], 1 keeps all; NULL: 1
+ *   min_p       : float[rows], in [0, 1]; NULL: 0
+ *   u           : double[rows], in [0, 1)
+ *   ids         : int32[rows] out
+ *   prob        : optional float[rows] out, the weight of the drawn token over that of all kept
+ * A row whose logits are all -inf gives id -1 and prob 0; a row that holds a NaN, or has a
+ * parameter outside its range, gives id -1 and prob NaN; where some logits are +inf, they have
+ * weight 1 and all others 0.  Decisions do not depend on the order of summation: weights are
+ * held as 64-bit integers, exp rounded to 2^-40 of the largest weight (a token below 2^-41 of it
+ * is not drawn), and all sums are exact.  V <= FGMM_SAMPLE_MAX_V (FGMM_ERR_UNSUPPORTED above);
+ * rows = 0 does nothing. */
+#define FGMM_SAMPLE_MAX_V (1 << 22)
+int fgmm_sample_logits(const void* logits, int dtype, int64_t rows, int V, int64_t ld,
+                       const float* temperature, const int32_t* top_k, const float* top_p,
+                       const float* min_p, const double* u, int32_t* ids, float* prob,
+                       fgmm_stream_t stream);
+
 /* Kernel timing, for benchmarks.  When enabled, the library records a CUDA
  * event pair on the call's stream around every kernel it launches and keeps a
  * launch counter; fgmm_profile_read synchronises the device, sums the elapsed

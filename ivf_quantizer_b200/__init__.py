@@ -9,6 +9,8 @@ streams.
 from ._lib import (BF16, CHUNK_POINTS, COV_DIAG, COV_SPHERICAL, EMPTY_NK, F32, MAX_TOP_M, PREC_AUTO,
                    PREC_FP16, PREC_FP16X3, PREC_FP32, FgmmError)
 from .gmm import GMM, stats_sum
+from .mx4 import MX4
+from .sample import sample_logits
 
-__all__ = ["GMM", "stats_sum", "CHUNK_POINTS", "FgmmError", "COV_DIAG", "COV_SPHERICAL", "PREC_FP32", "PREC_FP16X3",
+__all__ = ["GMM", "MX4", "sample_logits", "stats_sum", "CHUNK_POINTS", "FgmmError", "COV_DIAG", "COV_SPHERICAL", "PREC_FP32", "PREC_FP16X3",
            "PREC_FP16", "PREC_AUTO", "F32", "BF16", "MAX_TOP_M", "EMPTY_NK"]

@@ -21,6 +21,10 @@ READ_FN = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_OOM, ERR_NUMERIC, ERR_TIMEOUT, ERR_IO = range(8)
 MAX_TOP_M = 16
 IVF_MAX_TOPK = 32
+MX4_BLOCK = 32
+MX4_MAX_ROWS = (1 << 31) - 1024
+MX4_MAX_D = 1 << 20
+SAMPLE_MAX_V = 1 << 22
 STATIC_MAX_KD = 1 << 18
 STATIC_MAX_K = 1 << 14
 EMPTY_NK = 1e-6
@@ -83,6 +87,14 @@ SIGNATURES = {
     "fgmm_kmeans_step": (_int, [_vp, _vp, _int, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
     "fgmm_kmeans_seed": (_int, [_vp, _vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
     "fgmm_kmeans_seed_scratch_bytes": (_c.c_size_t, [_i64]),
+    "fgmm_mx4_codes_bytes": (_c.c_size_t, [_i64, _int]),
+    "fgmm_mx4_scales_bytes": (_c.c_size_t, [_i64, _int]),
+    "fgmm_mx4_encode": (_int, [_vp, _int, _i64, _int, _i64, _vp, _vp, _vp]),
+    "fgmm_mx4_decode": (_int, [_vp, _vp, _i64, _int, _vp, _int, _i64, _vp]),
+    "fgmm_mx4_scores": (_int, [_vp, _vp, _i64, _vp, _vp, _i64, _int, _flt, _vp, _vp, _int, _i64,
+                               _vp, _vp]),
+    "fgmm_sample_logits": (_int, [_vp, _int, _i64, _int, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                  _vp]),
     "fgmm_em_step_host": (_int, [_vp, _vp, _int, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
     "fgmm_em_partial_host": (_int, [_vp, _vp, _int, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
     "fgmm_em_step_reader": (_int, [_vp, _vp, _vp, _int, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),

@@ -182,6 +182,11 @@ int map_cuda(cudaError_t e) {
   return FGMM_ERR_CUDA;
 }
 
+// Codes and scales as every fgmm_mx4 call wants them.
+bool mx4_aligned(const uint8_t* codes, const uint8_t* scales) {
+  return codes && scales && ((uintptr_t)codes | (uintptr_t)scales) % 16 == 0;
+}
+
 void free_ws(Workspace& w) {
   void* ptrs[] = {w.mu,     w.prec,   w.cconst, w.logz, w.ll_tiles, w.ll_total,
                   w.stats,  w.nk,     w.status, w.center, w.dscale, w.wop,
@@ -1040,6 +1045,69 @@ int fgmm_ivf_search(int K, int D, const float* centroids, const int64_t* offsets
   if (nq == 0) return FGMM_OK;
   return map_cuda(launch_ivf_search(K, D, centroids, offsets, entries, X, ldx, Q, nq, ldq, nprobe,
                                     topk, out_ids, out_dist, dco_out, (cudaStream_t)stream));
+}
+
+size_t fgmm_mx4_codes_bytes(int64_t N, int D) {
+  if (N < 1 || D < 1 || N > FGMM_MX4_MAX_ROWS || D > FGMM_MX4_MAX_D) return 0;
+  return (size_t)N * ((D + 31) / 32) * 16;
+}
+
+size_t fgmm_mx4_scales_bytes(int64_t N, int D) {
+  if (N < 1 || D < 1 || N > FGMM_MX4_MAX_ROWS || D > FGMM_MX4_MAX_D) return 0;
+  return (size_t)((N + 127) / 128) * ((D + 127) / 128) * 512;
+}
+
+int fgmm_mx4_encode(const void* X, int x_dtype, int64_t N, int D, int64_t ldx, uint8_t* codes,
+                    uint8_t* scales, fgmm_stream_t stream) {
+  if (N < 0 || D < 1 || ldx < D || (x_dtype != FGMM_F32 && x_dtype != FGMM_BF16))
+    return FGMM_ERR_INVALID_ARG;
+  if (N > FGMM_MX4_MAX_ROWS || D > FGMM_MX4_MAX_D) return FGMM_ERR_UNSUPPORTED;
+  if (N == 0) return FGMM_OK;
+  if (!X || !mx4_aligned(codes, scales) || (uintptr_t)X % (x_dtype == FGMM_F32 ? 4 : 2))
+    return FGMM_ERR_INVALID_ARG;
+  return map_cuda(launch_mx4_encode(X, x_dtype, N, D, ldx, codes, scales, (cudaStream_t)stream));
+}
+
+int fgmm_mx4_decode(const uint8_t* codes, const uint8_t* scales, int64_t N, int D, void* out,
+                    int out_dtype, int64_t ldo, fgmm_stream_t stream) {
+  if (N < 0 || D < 1 || ldo < D || (out_dtype != FGMM_F32 && out_dtype != FGMM_BF16))
+    return FGMM_ERR_INVALID_ARG;
+  if (N > FGMM_MX4_MAX_ROWS || D > FGMM_MX4_MAX_D) return FGMM_ERR_UNSUPPORTED;
+  if (N == 0) return FGMM_OK;
+  if (!out || !mx4_aligned(codes, scales) || (uintptr_t)out % (out_dtype == FGMM_F32 ? 4 : 2))
+    return FGMM_ERR_INVALID_ARG;
+  return map_cuda(launch_mx4_decode(codes, scales, N, D, out, out_dtype, ldo,
+                                    (cudaStream_t)stream));
+}
+
+int fgmm_mx4_scores(const uint8_t* q_codes, const uint8_t* q_scales, int64_t M,
+                    const uint8_t* codes, const uint8_t* scales, int64_t N, int D, float alpha,
+                    const float* bias, void* out, int out_dtype, int64_t ldo, int* status,
+                    fgmm_stream_t stream) {
+  if (M < 0 || N < 0 || D < 1 || ldo < N || (out_dtype != FGMM_F32 && out_dtype != FGMM_BF16))
+    return FGMM_ERR_INVALID_ARG;
+  if (M > FGMM_MX4_MAX_ROWS || N > FGMM_MX4_MAX_ROWS || D > FGMM_MX4_MAX_D)
+    return FGMM_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return FGMM_OK;
+  if (!out || !mx4_aligned(q_codes, q_scales) || !mx4_aligned(codes, scales) ||
+      (uintptr_t)out % (out_dtype == FGMM_F32 ? 4 : 2) || (uintptr_t)bias % 4)
+    return FGMM_ERR_INVALID_ARG;
+  return map_cuda(launch_mx4_scores(q_codes, q_scales, M, codes, scales, N, D, alpha, bias, out,
+                                    out_dtype, ldo, status, (cudaStream_t)stream));
+}
+
+int fgmm_sample_logits(const void* logits, int dtype, int64_t rows, int V, int64_t ld,
+                       const float* temperature, const int32_t* top_k, const float* top_p,
+                       const float* min_p, const double* u, int32_t* ids, float* prob,
+                       fgmm_stream_t stream) {
+  if (rows < 0 || V < 1 || ld < V || (dtype != FGMM_F32 && dtype != FGMM_BF16))
+    return FGMM_ERR_INVALID_ARG;
+  if (V > FGMM_SAMPLE_MAX_V || rows > INT32_MAX) return FGMM_ERR_UNSUPPORTED;
+  if (rows == 0) return FGMM_OK;
+  if (!logits || !u || !ids || (uintptr_t)logits % (dtype == FGMM_F32 ? 4 : 2))
+    return FGMM_ERR_INVALID_ARG;
+  return map_cuda(launch_sample_logits(logits, dtype, rows, V, ld, temperature, top_k, top_p,
+                                       min_p, u, ids, prob, (cudaStream_t)stream));
 }
 
 const char* fgmm_profile_kernel_name(int index) {

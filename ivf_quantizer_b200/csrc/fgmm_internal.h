@@ -263,6 +263,20 @@ cudaError_t launch_ivf_search(int K, int D, const float* C, const int64_t* offse
                               const int64_t* entries, const float* X, int64_t ldx, const float* Q,
                               int64_t nq, int64_t ldq, int nprobe, int topk, int64_t* out_i,
                               float* out_d, int64_t* dco, cudaStream_t s);
+// 4-bit codes (fgmm_mx4.cu)
+cudaError_t launch_mx4_encode(const void* X, int x_dtype, int64_t n, int D, int64_t ldx,
+                              uint8_t* codes, uint8_t* scales, cudaStream_t s);
+cudaError_t launch_mx4_decode(const uint8_t* codes, const uint8_t* scales, int64_t n, int D,
+                              void* out, int out_dtype, int64_t ldo, cudaStream_t s);
+cudaError_t launch_mx4_scores(const uint8_t* q_codes, const uint8_t* q_scales, int64_t m,
+                              const uint8_t* codes, const uint8_t* scales, int64_t n, int D,
+                              float alpha, const float* bias, void* out, int out_dtype,
+                              int64_t ldo, int* status, cudaStream_t s);
+// draws from truncated softmaxes (fgmm_sample.cu)
+cudaError_t launch_sample_logits(const void* logits, int dtype, int64_t rows, int V, int64_t ld,
+                                 const float* temperature, const int32_t* top_k,
+                                 const float* top_p, const float* min_p, const double* u,
+                                 int32_t* ids, float* prob, cudaStream_t s);
 // k-means warm start (fgmm_kmeans.cu)
 size_t kmeans_seed_scratch_bytes(int64_t n);
 cudaError_t launch_kmeans_step(const Ctx& c, const void* X, int x_dtype, int64_t n, int64_t ldx,

@@ -1,0 +1,108 @@
+"""``MX4``: vectors held as 4-bit codes (OCP Microscaling Formats v1.0, MXFP4: blocks of 32
+values with one power-of-two scale) and the scores of queries against them, through
+fgmm_mx4_encode / fgmm_mx4_decode / fgmm_mx4_scores (include/fgmm.h).  CUDA tensors only;
+argument marshalling only.  Work runs on the current stream of the tensors' device."""
+from __future__ import annotations
+
+import torch
+
+from . import _lib
+from ._lib import LIB, check
+
+_DTYPES = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16}
+
+
+def on_device(t: torch.Tensor):
+    """(guard, stream) for a call on t's device: the guard makes it the current one."""
+    return torch.cuda.device(t.device), torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _rows(X: torch.Tensor, what: str):
+    if not (isinstance(X, torch.Tensor) and X.is_cuda and X.dim() == 2):
+        raise ValueError(f"{what} must be a 2-D CUDA tensor")
+    if X.dtype not in _DTYPES:
+        raise TypeError(f"{what} must be float32 or bfloat16")
+    if X.shape[1] < 1:
+        raise ValueError(f"{what} must have at least one dimension")
+    if X.shape[1] > 1 and X.stride(1) != 1 or X.shape[0] > 1 and X.stride(0) < X.shape[1]:
+        raise ValueError(f"{what} rows must be contiguous and must not overlap")
+    return _DTYPES[X.dtype], max(X.stride(0), X.shape[1])
+
+
+class MX4:
+    """The rows of X [N, D] (float32 or bfloat16) as 4-bit codes: 4.25 bits a value.
+
+    codes  : uint8 [N, ceil(D / 32) * 16], two codes a byte
+    scales : uint8, tiles of 128 rows x 4 blocks as include/fgmm.h describes
+    """
+
+    def __init__(self, X: torch.Tensor):
+        dt, ldx = _rows(X, "X")
+        N, D = X.shape
+        self.shape = (N, D)
+        self.codes, self.scales = self._empty(N, D, X.device)
+        guard, stream = on_device(X)
+        with guard:
+            check(LIB.fgmm_mx4_encode(X.data_ptr(), dt, N, D, ldx, self.codes.data_ptr(),
+                                      self.scales.data_ptr(), stream), "fgmm_mx4_encode")
+
+    @staticmethod
+    def _empty(N, D, device):
+        nb = -(-D // _lib.MX4_BLOCK)
+        return (torch.empty(N, nb * 16, dtype=torch.uint8, device=device),
+                torch.empty(-(-N // 128) * -(-nb // 4) * 512, dtype=torch.uint8, device=device))
+
+    @classmethod
+    def from_codes(cls, codes: torch.Tensor, scales: torch.Tensor, D: int) -> "MX4":
+        """Codes made earlier (kept by reference)."""
+        if not (codes.is_cuda and scales.device == codes.device
+                and codes.dtype == scales.dtype == torch.uint8 and codes.is_contiguous()
+                and scales.is_contiguous() and codes.dim() == 2):
+            raise ValueError("codes [N, bytes] and scales must be contiguous uint8 tensors on one GPU")
+        N, nb = codes.shape[0], -(-D // _lib.MX4_BLOCK)
+        if D < 1 or codes.shape[1] != nb * 16 or scales.numel() != -(-N // 128) * -(-nb // 4) * 512:
+            raise ValueError("codes or scales have the wrong size for this D")
+        self = cls.__new__(cls)
+        self.shape, self.codes, self.scales = (N, D), codes, scales
+        return self
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+    def decode(self, dtype: torch.dtype = torch.float32) -> torch.Tensor:
+        """The rows that the codes stand for, [N, D], float32 or bfloat16 (exact in both)."""
+        if dtype not in _DTYPES:
+            raise TypeError("dtype must be float32 or bfloat16")
+        N, D = self.shape
+        out = torch.empty(N, D, dtype=dtype, device=self.codes.device)
+        guard, stream = on_device(out)
+        with guard:
+            check(LIB.fgmm_mx4_decode(self.codes.data_ptr(), self.scales.data_ptr(), N, D,
+                                      out.data_ptr(), _DTYPES[dtype], D, stream), "fgmm_mx4_decode")
+        return out
+
+    def scores(self, queries, alpha: float = 1.0, bias: torch.Tensor | None = None,
+               dtype: torch.dtype = torch.float32) -> torch.Tensor:
+        """alpha * queries @ rows.T + bias, [M, N].  queries: an MX4, or a [M, D] tensor, which
+        is encoded first.  bias: float32 [N]."""
+        q = queries if isinstance(queries, MX4) else MX4(queries)
+        (M, D), N = q.shape, self.shape[0]
+        if D != self.shape[1]:
+            raise ValueError(f"queries have {D} dimensions, the codes {self.shape[1]}")
+        dev = self.codes.device
+        if q.codes.device != dev:
+            raise ValueError("queries and codes must be on one device")
+        if dtype not in _DTYPES:
+            raise TypeError("dtype must be float32 or bfloat16")
+        if bias is not None and not (bias.device == dev and bias.dtype == torch.float32
+                                     and bias.shape == (N,) and bias.is_contiguous()):
+            raise ValueError("bias must be a contiguous float32 [N] tensor on the codes' device")
+        out = torch.empty(M, N, dtype=dtype, device=dev)
+        guard, stream = on_device(out)
+        with guard:
+            check(LIB.fgmm_mx4_scores(q.codes.data_ptr(), q.scales.data_ptr(), M,
+                                      self.codes.data_ptr(), self.scales.data_ptr(), N, D, alpha,
+                                      None if bias is None else bias.data_ptr(), out.data_ptr(),
+                                      _DTYPES[dtype], N, None, stream), "fgmm_mx4_scores")
+        return out
