@@ -8,6 +8,7 @@
 #include <cuda_bf16.h>
 
 #include "fgmm_internal.h"
+#include "sm100_ptx.cuh"
 
 namespace fgmm {
 namespace {
@@ -175,63 +176,271 @@ __global__ void __launch_bounds__(kMxThreads)
   }
 }
 
-// Scores on CUDA cores: a 64 x 64 tile of outputs a CTA, one block of 32 dimensions at a time
-// decoded into shared memory, 4 x 4 outputs a thread.
-template <typename T>
-__global__ void __launch_bounds__(256)
-    mx4_scores_simt_kernel(const uint8_t* __restrict__ qc, const uint8_t* __restrict__ qs, int64_t m,
-                           const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs,
-                           int64_t n, int nb, float alpha, const float* __restrict__ bias,
-                           T* __restrict__ out, int64_t ldo, int64_t ntiles_n) {
-  __shared__ float sq[32][68], sx[32][68];
-  const int nkc = (nb + 3) / 4;
-  const int64_t m0 = (int64_t)(blockIdx.x / ntiles_n) * 64, n0 = (blockIdx.x % ntiles_n) * 64;
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  float acc[4][4] = {};
-  for (int b = 0; b < nb; ++b) {
-    // thread: 8 codes of one row of each side
-    const int r = tid >> 2, part = tid & 3;
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const int64_t row = (side ? n0 : m0) + r;
-      const uint8_t* codes = side ? xc : qc;
-      const uint8_t* scales = side ? xs : qs;
-      float v[8] = {};
-      if (row < (side ? n : m)) {
-        const float s = mx_scale(scales[((row >> 7) * nkc + (b >> 2)) * 512 + (row & 31) * 16 +
-                                        ((row & 127) >> 5) * 4 + (b & 3)]);
-        const uint32_t c = *reinterpret_cast<const uint32_t*>(codes + row * ((int64_t)nb * 16) +
-                                                              b * 16 + part * 4);
-        float lo[4], hi[4];
-        mx_values4(c, lo);
-        mx_values4(c >> 16, hi);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = lo[j] * s, v[4 + j] = hi[j] * s;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) (side ? sx : sq)[part * 8 + j][r] = v[j];
+// ------------------------------------------------------------------ scores (tcgen05)
+// The vectors are the M side of the products (128 of them a tile: TMEM lane = vector), the
+// queries the N side (NT a tile: TMEM column = query).  The codes then stream through the wide
+// side whatever the number of queries, and a warp's 32 lanes write 32 consecutive scores of one
+// query: whole 128-byte lines from registers, for any N and any row stride.
+//
+// One CTA a SM walks its tiles: a TMA warp fills a ring of stages (256 dimensions of 128 vectors
+// and NT queries, 128 bytes a row, and their scale tiles), one thread copies a stage's scales to
+// TMEM and issues its four K = 64 block-scaled products, and the epilogue warps drain one of two
+// accumulators while the other is filled.
+constexpr int kMxBM = 128;         // vectors a tile
+constexpr int kMxRowB = 128;       // bytes of a row in a stage: 256 dimensions
+constexpr int kMxSfB = 1024;       // scale bytes of 128 rows in a stage: two tiles of 512
+
+template <int NT>
+struct MxCfg {
+  static constexpr int kStage = kMxBM * kMxRowB + NT * kMxRowB + 2 * kMxSfB;
+  static constexpr int kStages = (216 * 1024) / kStage < 10 ? (216 * 1024) / kStage : 10;
+  static constexpr int kEpiWarps = NT >= 64 ? 8 : 4;
+  static constexpr int kThreads = 128 + 32 * kEpiWarps;
+  static constexpr int kCols = NT == 128 ? 512 : 4 * NT < 64 ? 64 : 4 * NT;  // TMEM columns
+  static constexpr int kSfCol = 2 * NT;             // two scale sets of 16 columns behind the sums
+};
+
+struct MxBars {
+  uint64_t full[10], empty[10], s_full[2], s_empty[2], drain;
+  uint32_t tmem;
+  int abort;
+};
+
+__device__ __forceinline__ void mx_timeout(int* status, MxBars* bars) {
+  if (status) atomicCAS(status, FGMM_OK, FGMM_ERR_TIMEOUT);
+  bars->abort = 1;
+}
+
+template <int NT, typename T>
+__global__ void __launch_bounds__(MxCfg<NT>::kThreads, 1)
+    mx4_scores_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmq,
+                      const uint8_t* __restrict__ xs, const uint8_t* __restrict__ qs, int64_t n,
+                      int64_t m, int nb, int64_t ntiles, int mtiles, float alpha,
+                      const float* __restrict__ bias, T* __restrict__ out, int64_t ldo, int* status) {
+  using C = MxCfg<NT>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* ring = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  MxBars* bars = reinterpret_cast<MxBars*>(ring + C::kStages * C::kStage);
+  volatile int* abort = &bars->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nkc = (nb + 3) / 4;                     // scale tiles (128 dimensions) of a row
+  const int nst = (nkc + 1) / 2;                    // stages of a tile
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      ptx::mbar_init(&bars->full[s], 1);
+      ptx::mbar_init(&bars->empty[s], 1);
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      float a[4], c[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) a[j] = sq[k][ty * 4 + j], c[j] = sx[k][tx + 16 * j];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], c[j], acc[i][j]);
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(&bars->s_full[b], 1);
+      ptx::mbar_init(&bars->s_empty[b], C::kEpiWarps);
     }
-    __syncthreads();
+    ptx::mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    ptx::fence_mbar_init();
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t row = m0 + ty * 4 + i, col = n0 + tx + 16 * j;
-      if (row < m && col < n)
-        mx_st(out + row * ldo + col, fmaf(alpha, acc[i][j], bias ? bias[col] : 0.f));
+  if (warp == 1) {
+    ptx::tmem_alloc(&bars->tmem, C::kCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      ptx::prefetch_tmap(&tmx);
+      ptx::prefetch_tmap(&tmq);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int64_t t = blockIdx.x; ok && t < ntiles && !*abort; t += gridDim.x) {
+        const int64_t nt = t / mtiles;
+        const int mt = (int)(t - nt * mtiles);
+        for (int k = 0; k < nst; ++k, ++it) {
+          const int s = it % C::kStages;
+          if (it >= C::kStages && !ptx::mbar_wait(&bars->empty[s], ((it / C::kStages) - 1) & 1, abort)) {
+            mx_timeout(status, bars);
+            ok = false;
+            break;
+          }
+          unsigned char* a = ring + s * C::kStage;
+          unsigned char* b = a + kMxBM * kMxRowB;
+          unsigned char* sf = b + NT * kMxRowB;
+          const uint32_t sfb = (nkc - 2 * k >= 2 ? 2 : 1) * 512;
+          ptx::mbar_arrive_expect_tx(&bars->full[s], kMxBM * kMxRowB + NT * kMxRowB + 2 * sfb);
+          ptx::tma_load_2d(a, &tmx, &bars->full[s], k * kMxRowB, (int)(nt * kMxBM));
+          ptx::bulk_load(sf, xs + (nt * nkc + 2 * k) * 512, sfb, &bars->full[s]);
+          ptx::tma_load_2d(b, &tmq, &bars->full[s], k * kMxRowB, mt * NT);
+          ptx::bulk_load(sf + kMxSfB, qs + ((int64_t)mt * nkc + 2 * k) * 512, sfb, &bars->full[s]);
+        }
+      }
+      if (*abort)  // let every copy this thread started land before the CTA exits
+        for (uint32_t k = (it > C::kStages ? it - C::kStages : 0); k < it; ++k)
+          ptx::mbar_drain(&bars->full[k % C::kStages], (k / C::kStages) & 1);
     }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint64_t kHiK = ptx::sw128_hi(16, 1024);
+      uint32_t it = 0, j = 0;
+      bool ok = true;
+      for (int64_t t = blockIdx.x; ok && t < ntiles && !*abort; t += gridDim.x, ++j) {
+        const uint32_t buf = j & 1;
+        if (j >= 2 && !ptx::mbar_wait(&bars->s_empty[buf], ((j >> 1) - 1) & 1, abort)) {
+          ok = false;
+          break;
+        }
+        const uint32_t d_tmem = tmem + buf * NT;
+        for (int k = 0; k < nst; ++k, ++it) {
+          const int s = it % C::kStages;
+          if (!ptx::mbar_wait(&bars->full[s], (it / C::kStages) & 1, abort)) {
+            ok = false;
+            break;
+          }
+          const uint32_t a = ptx::smem_u32(ring + s * C::kStage);
+          const uint32_t b = a + kMxBM * kMxRowB, sf = b + NT * kMxRowB;
+          const uint32_t sft = tmem + C::kSfCol + (it & 1) * 16;
+          const int steps = min(4, (nb + 1) / 2 - 4 * k);
+          for (int h = 0; h < (steps + 1) / 2; ++h) {
+            ptx::tmem_cp_32x128(sft + 4 * h, ptx::rows16_desc(sf + 512 * h));
+            ptx::tmem_cp_32x128(sft + 8 + 4 * h, ptx::rows16_desc(sf + kMxSfB + 512 * h));
+          }
+          const uint64_t da = ptx::sw128_desc(a, kHiK), db = ptx::sw128_desc(b, kHiK);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (q < steps)
+              ptx::mma_mxf4_ss(d_tmem, da + 2 * q, db + 2 * q, ptx::idesc_mxf4(kMxBM, NT, 2 * (q & 1)),
+                               sft + 4 * (q >> 1), sft + 8 + 4 * (q >> 1), k > 0 || q > 0);
+          ptx::mma_commit(&bars->empty[s]);
+        }
+        if (ok) ptx::mma_commit(&bars->s_full[buf]);
+      }
+      if (!ok) mx_timeout(status, bars);
+      if (*abort) {  // wait for the products already issued before TMEM is freed
+        ptx::mma_commit(&bars->drain);
+        ptx::mbar_drain(&bars->drain, 0);
+      }
+    }
+  } else if (warp >= 4) {
+    constexpr int kColsWarp = NT * 4 / C::kEpiWarps;          // columns a warp drains
+    constexpr int kChunk32 = kColsWarp < 32 ? 16 : 32;
+    const int q = warp & 3, c0 = ((warp - 4) >> 2) * kColsWarp;
+    const uint32_t lane_base = (uint32_t)(q * 32) << 16;
+    uint32_t j = 0;
+    for (int64_t t = blockIdx.x; t < ntiles && !*abort; t += gridDim.x, ++j) {
+      const int64_t nt = t / mtiles;
+      const int64_t m0 = (t - nt * mtiles) * NT;
+      const uint32_t buf = j & 1;
+      const int64_t row = nt * kMxBM + q * 32 + lane;
+      const float bv = bias && row < n ? __ldg(bias + row) : 0.f;
+      if (!ptx::mbar_wait_warp(&bars->s_full[buf], (j >> 1) & 1, abort)) {
+        mx_timeout(status, bars);
+        break;
+      }
+      ptx::tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < kColsWarp; c += kChunk32) {
+        uint32_t u[kChunk32];
+        if constexpr (kChunk32 == 32) ptx::tmem_ld32(tmem + lane_base + buf * NT + c0 + c, u);
+        else ptx::tmem_ld16(tmem + lane_base + buf * NT + c0 + c, u);
+        ptx::tmem_wait_ld();
+        if (c + kChunk32 == kColsWarp) {  // all in registers: hand the accumulator back
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&bars->s_empty[buf]);
+        }
+        const int64_t mc = m0 + c0 + c;
+        T* p = out + mc * ldo + row;
+        if (row < n) {
+          if (mc + kChunk32 <= m) {
+#pragma unroll
+            for (int e = 0; e < kChunk32; ++e, p += ldo) mx_st(p, fmaf(alpha, __uint_as_float(u[e]), bv));
+          } else {
+#pragma unroll
+            for (int e = 0; e < kChunk32; ++e, p += ldo)
+              if (mc + e < m) mx_st(p, fmaf(alpha, __uint_as_float(u[e]), bv));
+          }
+        }
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, C::kCols);
+  }
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn mx_encode_tiled() {
+  static EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
+                       cudaSuccess && q == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<EncodeTiledFn>(p) : nullptr;
+  }();
+  return fn;
+}
+
+// Rows of codes as boxes of 128 bytes x `box_rows`; what lies beyond a row or the last row is 0.
+bool mx_tmap(CUtensorMap* map, const uint8_t* codes, int nb, int64_t rows, int box_rows) {
+  EncodeTiledFn enc = mx_encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)nb * 16, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)nb * 16};
+  const cuuint32_t box[2] = {kMxRowB, (cuuint32_t)box_rows};
+  const cuuint32_t one[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, box,
+             one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct MxArgs {
+  const uint8_t *qc, *qs, *xc, *xs;
+  int64_t m, n;
+  int nb;
+  float alpha;
+  const float* bias;
+  void* out;
+  int64_t ldo;
+  int* status;
+  cudaStream_t s;
+};
+
+template <int NT, typename T>
+cudaError_t mx_scores(const MxArgs& a) {
+  using C = MxCfg<NT>;
+  static_assert(C::kStages >= 4 && C::kStages <= 10 && C::kSfCol + 32 <= C::kCols, "tile");
+  constexpr int smem = 1024 + C::kStages * C::kStage + (int)sizeof(MxBars);
+  static_assert(smem <= 227 * 1024, "shared memory");
+  CUtensorMap tmx, tmq;
+  if (!mx_tmap(&tmx, a.xc, a.nb, a.n, kMxBM) || !mx_tmap(&tmq, a.qc, a.nb, a.m, NT))
+    return cudaErrorInvalidValue;
+  auto* k = mx4_scores_kernel<NT, T>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  int dev = 0, sms = 0;
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int64_t mt = (a.m + NT - 1) / NT, tiles = (a.n + kMxBM - 1) / kMxBM * mt;
+  k<<<(unsigned)(tiles < sms ? tiles : sms), C::kThreads, smem, a.s>>>(
+      tmx, tmq, a.xs, a.qs, a.n, a.m, a.nb, tiles, (int)mt, a.alpha, a.bias, static_cast<T*>(a.out),
+      a.ldo, a.status);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t mx_scores_nt(const MxArgs& a) {
+  if (a.m <= 16) return mx_scores<16, T>(a);
+  if (a.m <= 32) return mx_scores<32, T>(a);
+  if (a.m <= 64) return mx_scores<64, T>(a);
+  return mx_scores<128, T>(a);
 }
 
 unsigned mx_grid(int64_t groups) {
@@ -284,18 +493,9 @@ cudaError_t launch_mx4_scores(const uint8_t* q_codes, const uint8_t* q_scales, i
                               const uint8_t* codes, const uint8_t* scales, int64_t n, int D,
                               float alpha, const float* bias, void* out, int out_dtype,
                               int64_t ldo, int* status, cudaStream_t s) {
-  (void)status;
-  const int nb = (D + 31) / 32;
-  const int64_t tn = (n + 63) / 64, tiles = tn * ((m + 63) / 64);
-  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-  if (out_dtype == FGMM_F32)
-    mx4_scores_simt_kernel<float><<<(unsigned)tiles, 256, 0, s>>>(
-        q_codes, q_scales, m, codes, scales, n, nb, alpha, bias, static_cast<float*>(out), ldo, tn);
-  else
-    mx4_scores_simt_kernel<__nv_bfloat16><<<(unsigned)tiles, 256, 0, s>>>(
-        q_codes, q_scales, m, codes, scales, n, nb, alpha, bias, static_cast<__nv_bfloat16*>(out),
-        ldo, tn);
-  return cudaGetLastError();
+  const MxArgs a = {q_codes, q_scales, codes, scales, m, n, (D + 31) / 32, alpha, bias, out, ldo,
+                    status, s};
+  return out_dtype == FGMM_F32 ? mx_scores_nt<float>(a) : mx_scores_nt<__nv_bfloat16>(a);
 }
 
 }  // namespace fgmm

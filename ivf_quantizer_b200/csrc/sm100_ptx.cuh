@@ -178,6 +178,26 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
+// D[tmem] (+)= A[smem desc] x B[smem desc], kind::mxf4: e2m1 operands, K = 64 a product, one
+// e8m0 scale per 32 of K for every row of A and of B in tensor memory (two of them a product).
+__device__ __forceinline__ void mma_mxf4_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], "
+      "p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+      : "memory");
+}
+
+// Copy 512 bytes of shared memory (32 rows of 16 bytes) to four TMEM columns: row l to lane l of
+// every warp's lane quarter.  Executes in order with the tcgen05.mma of the same thread.
+__device__ __forceinline__ void tmem_cp_32x128(uint32_t taddr, uint64_t s_desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc)
+               : "memory");
+}
+
 // Arrive on an mbarrier once every previously issued tcgen05.mma of this thread completes.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile(
@@ -299,6 +319,21 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn_major, 
          | (0u << 7) | (0u << 10)        // A, B format f16
          | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// kind::mxf4 instruction descriptor: A, B e2m1 K-major, scales e8m0; sf selects which two of the
+// four scale bytes of a TMEM word apply (0: the lower, 2: the upper two), for A and B alike.
+//   [4,6) B scale id | [7,10) A fmt (1 = e2m1) | [10,12) B fmt | [17,23) N>>3 | [23] e8m0 |
+//   [27,29) M>>7 | [29,31) A scale id
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, uint32_t sf) {
+  return (sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
+         ((uint32_t)(M >> 7) << 27) | (sf << 29);
+}
+
+// Descriptor of an unswizzled matrix of 16-byte rows, 8-row groups of 128 contiguous bytes.
+__device__ __forceinline__ uint64_t rows16_desc(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)8 << 16) | ((uint64_t)8 << 32) |
+         ((uint64_t)1 << 46);
 }
 
 }  // namespace ptx
