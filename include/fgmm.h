@@ -467,7 +467,8 @@ int fgmm_mx4_scores(const uint8_t* q_codes, const uint8_t* q_scales, int64_t M,
  * their weight (a token stays when the weight before it is below top_p times the whole; the first
  * always stays); of these the tokens with w_i >= min_p.  The draw is the smallest index i at which
  * the running weight of the kept tokens, in index order, exceeds u times their whole weight.
- *   temperature : float[rows], >= 0 and finite; 0 takes the first maximum; NULL: 1
+ *   temperature : float[rows], >= 0 and finite; 0 takes the first maximum, what is between 0 and
+ *                 2^-80 counts as 2^-80; NULL: 1
  *   top_k       : int32[rows]; <= 0 or >= V keeps all; NULL: all
  *   top_p       : float[rows], in (0, 1], 1 keeps all; NULL: 1
  *   min_p       : float[rows], in [0, 1]; NULL: 0

@@ -8,13 +8,13 @@
 // The tokens that top-k, top-p and min-p keep are a prefix of the order (logit descending, index
 // ascending).  Tokens are numbered by that order with a 64-bit place (inverted key of the logit in
 // the upper half, index in the lower half), and a truncation is the place of the last kept token.
-// It is found by histograms: first over logits (bins of equal width down to weight 2^-41), then,
-// inside the bin that holds the border, over places, until so few tokens are left that they can be
-// ranked against one another.
+// It is found by a histogram over log2 weights (bins of 1/32 down to weight 2^-41); the tokens of
+// the bin that holds the border are sorted.  A bin too full for that is split by histograms over
+// places first.
 //
-// A cluster of C CTAs takes a row; each keeps its contiguous slice of the row in shared memory,
-// so the row is read once from memory.  Steps, each ending in an exchange over the cluster:
-//   maximum (while loading) | [histogram, border]  twice at most | kept weight of every warp's
+// A cluster of C CTAs takes a row, a contiguous slice each.  Steps, each ending in an exchange over
+// the cluster:
+//   maximum | [histogram, border]  for top-k, then for top-p | kept weight of every warp's
 //   contiguous part | the warp whose part holds the target finds the token by a scan.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -30,31 +30,32 @@ namespace cg = cooperative_groups;
 constexpr double kSmOne = 1099511627776.0;  // 2^40
 constexpr uint64_t kSmAll = ~0ull;          // border that keeps everything
 
-__device__ __forceinline__ float sm_ld(const float* p) { return __ldg(p); }
-__device__ __forceinline__ float sm_ld(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-
-// The values of 16 bytes of a row.
+// The values of 16 bytes of a row, in groups of four.
 template <typename T>
 struct SmVec;
 template <>
 struct SmVec<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ void get(const uint4& t, float (&v)[4]) {
+  static __device__ __forceinline__ void get(const uint4& t, int, float (&v)[4]) {
     v[0] = __uint_as_float(t.x), v[1] = __uint_as_float(t.y);
     v[2] = __uint_as_float(t.z), v[3] = __uint_as_float(t.w);
+  }
+  static __device__ __forceinline__ void put(uint32_t (&w)[4], int j, float x) {
+    w[j] = __float_as_uint(x);
   }
   static constexpr uint32_t kMinusInf = 0xff800000u;
 };
 template <>
 struct SmVec<__nv_bfloat16> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ void get(const uint4& t, float (&v)[8]) {
-    const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
+  static __device__ __forceinline__ void get(const uint4& t, int g, float (&v)[4]) {
+    const uint32_t a = g ? t.z : t.x, b = g ? t.w : t.y;
+    v[0] = __uint_as_float(a << 16), v[1] = __uint_as_float(a & 0xffff0000u);
+    v[2] = __uint_as_float(b << 16), v[3] = __uint_as_float(b & 0xffff0000u);
+  }
+  static __device__ __forceinline__ void put(uint32_t (&w)[4], int j, __nv_bfloat16 x) {
+    const uint32_t b = __bfloat16_as_ushort(x), at = 16 * (j & 1);
+    w[j >> 1] = (w[j >> 1] & ~(0xffffu << at)) | b << at;
   }
   static constexpr uint32_t kMinusInf = 0xff80ff80u;
 };
@@ -78,73 +79,126 @@ __device__ __forceinline__ float sm_max_nan(float a, float b) {
   return r;
 }
 
-// What a row's weights and bins need.
+// (double)x for a normal number: the conversion instruction runs at a quarter of the rate of fp64
+// arithmetic.  0 and subnormal logits read as less than 2^-126 in magnitude, which moves no weight;
+// infinity reads as 2^128, so that a row whose maximum is infinite needs no case of its own.
+__device__ __forceinline__ double sm_double(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return __hiloint2double((int)((b & 0x80000000u) | (((b & 0x7fffffffu) >> 3) + 0x38000000u)),
+                          (int)(b << 29));
+}
+
+// What a row's weights need.
 struct SmRow {
-  float top, half_top, bin_scale;
-  double topd, c;                           // c = log2(e) / T
+  float top, least;                         // logits below least weigh nothing (below 2^-41)
+  double topd, c;                           // c = 32 log2(e) / T
 };
 
-// round(2^40 2^y) for y = (x - top) c in [-42, 0], 2^40 for the maximum itself (infinite or not):
-// y = n + f with |f| <= 1/2, the Taylor series of 2^f to f^11 (remainder 2^-47), the exponent
-// n + 40 added to that of the sum, and the rounding done by adding 2^52.
-__device__ __forceinline__ uint64_t sm_weight(float x, const SmRow& r) {
-  const double y = ((double)x - r.topd) * r.c;
-  const double k = y + 6755399441055744.0;  // 1.5 2^52: the low word holds round(y)
-  const double f = y - (k - 6755399441055744.0);
-  double p = 4.4455382718708116e-10;        // ln(2)^11 / 11!
-  p = fma(p, f, 7.0549116208011234e-09);
-  p = fma(p, f, 1.0178086009239700e-07);
-  p = fma(p, f, 1.3215486790144310e-06);
-  p = fma(p, f, 1.5252733804059841e-05);
-  p = fma(p, f, 1.5403530393381609e-04);
-  p = fma(p, f, 1.3333558146428443e-03);
-  p = fma(p, f, 9.6181291076284769e-03);
-  p = fma(p, f, 5.5504108664821583e-02);
-  p = fma(p, f, 2.4022650695910072e-01);
-  p = fma(p, f, 6.9314718055994529e-01);
-  p = fma(p, f, 1.0);
-  const int n = __double2loint(k) + 40;
-  const double w = __hiloint2double(__double2hiint(p) + (n << 20), __double2loint(p));
-  const double m = w + 4503599627370496.0;  // 2^52: the mantissa holds round(w)
-  return x == r.top ? 1ull << 40 : (uint64_t)__double_as_longlong(m) & 0xfffffffffffffull;
-}
+constexpr double kSmMagic = 6755399441055744.0;  // 1.5 2^52: a sum's low word is the rounded integer
+constexpr float kSmColdest = 8.271806125530277e-25f;  // 2^-80: logits that differ by 2^-74 or more differ
+                                            // in weight by more than 2^-42 at any lower temperature too
+constexpr int kSmBins = 1344;               // 32 bins a factor of two, down to 2^-41.3 and 2^-42
 
-template <int NB>
+// -32 log2 of the weight of a logit above the floor, rounded: its bin.
 __device__ __forceinline__ int sm_bin(float x, const SmRow& r) {
-  // monotone in x; equal values of the maximum (infinite ones too: NaN converts to 0) give bin 0
-  const float d = fmaf(x, -0.5f, r.half_top) * r.bin_scale;
-  return (int)min(__float2uint_rz(d), (unsigned)(NB - 1));
+  return -__double2loint(fma(sm_double(x) - r.topd, r.c, kSmMagic));
+}
+// round(2^40 2^(y / 32)), y = (x - top) c in [-1322, 0]: y = n + f with |f| <= 1/2; 2^(f / 32) by its
+// Taylor series to f^5 (remainder 2^-48); table[j] = 2^(40 + j / 32), whose exponent takes n / 32;
+// the product is rounded by adding 2^52.  Ten fp64 operations.
+__device__ __forceinline__ uint64_t sm_weight(float x, const SmRow& r, const double* table, int& bin) {
+  const double d = sm_double(x) - r.topd;
+  const double k = fma(d, r.c, kSmMagic);
+  const double f = fma(d, r.c, kSmMagic - k);
+  double p = 3.97370998454941609e-11;       // (ln 2 / 32)^5 / 5!
+  p = fma(p, f, 9.17256270182464302e-09);
+  p = fma(p, f, 1.69385097243718210e-06);
+  p = fma(p, f, 2.34596198202246799e-04);
+  p = fma(p, f, 2.16608493924982902e-02);
+  p = fma(p, f, 1.0);
+  const int n = __double2loint(k);
+  const double t = table[n & 31];
+  const double m = fma(p, __hiloint2double(__double2hiint(t) + (n >> 5) * (1 << 20), __double2loint(t)),
+                       4503599627370496.0);
+  bin = -n;
+  return (uint64_t)__double_as_longlong(m) & 0xfffffffffffffull;
 }
 
-template <int THREADS, int NB>
+// The last place that min-p keeps: that of the smallest logit with (x - top) / T >= log(min_p), by
+// bisection over keys, at first round the nearest float to top + T log(min_p).
+__device__ __forceinline__ uint64_t sm_min_p(float mp, const SmRow& r) {
+  const double cut = log((double)mp) * 46.166241308446828;
+  auto in = [&](uint32_t key) {
+    const float x = sm_value(key);
+    return x == r.top || ((double)x - (double)r.top) * r.c >= cut;
+  };
+  const uint32_t lowest = 0x007fffffu, top_key = sm_key(r.top);   // key of -inf: never in
+  const uint32_t guess = sm_key((float)fmax((double)r.top + cut / r.c, -3.4e38));
+  uint32_t lo = guess > lowest + 4 && !in(guess - 4) ? guess - 4 : lowest;
+  uint32_t hi = guess < top_key - 4 && in(guess + 4) ? guess + 4 : top_key;
+  while (hi - lo > 1) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    if (in(mid)) hi = mid;
+    else lo = mid;
+  }
+  return (uint64_t)(~hi) << 32 | 0xffffffffu;
+}
+// Bounds of a row's parameters (NaN fails them).
+__device__ __forceinline__ bool sm_valid(float t, float p, float mp, double u) {
+  return t >= 0.f && t < CUDART_INF_F && p > 0.f && p <= 1.f && mp >= 0.f && mp <= 1.f && u >= 0.0 &&
+         u < 1.0;
+}
+__device__ __forceinline__ SmRow sm_row(float top, float t) {
+  SmRow r;
+  r.top = top;
+  r.topd = sm_double(top);
+  r.c = t > 0.f ? 46.166241308446828 / (double)t : 0.0;
+  r.least = fminf(__double2float_ru((double)top - 28.62 * (double)t), top);
+  return r;
+}
+__device__ __forceinline__ float sm_prob(float x, float top, float t, uint64_t total) {
+  if (t == 0.f) return 1.f;
+  return (float)((x == top ? 1.0 : exp(((double)x - (double)top) / (double)t)) * kSmOne / (double)total);
+}
+
+constexpr int kSmList = 2048;               // tokens of a border bin that are sorted
+
+template <int THREADS>
 struct SmShared {
-  static constexpr int kWarps = THREADS / 32, kCap = THREADS < 256 ? THREADS : 256;
-  uint32_t lo[NB], hi[NB], cnt[NB];         // this CTA's histogram (mass in two words, number)
-  uint64_t m0[NB], m1[NB];                  // the cluster's: over logits, over places
-  uint32_t c0[NB], c1[NB];
-  uint64_t list[kCap];
+  static constexpr int kWarps = THREADS / 32;
+  uint4 ends[2];
+  // this CTA's histogram (mass in two words, number); then, in CTA 0, the list that is sorted
+  union {
+    struct { uint32_t lo[kSmBins], hi[kSmBins], cnt[kSmBins]; } h;
+    uint64_t list[THREADS < 512 ? 1024 : kSmList];
+  };
+  uint64_t m0[kSmBins];                     // the cluster's
+  uint32_t c0[kSmBins];
+  double table[32];
   uint64_t wsum[kWarps], wmass[kWarps];
   uint32_t wcnt[kWarps];
   float wmax[kWarps];
-  float part_max;
+  float part_max[8];
   uint64_t part_lo, part_hi;
-  uint64_t above_mass, out_place, out_mass;
-  uint32_t above_cnt, bin_cnt, nlist;
+  uint64_t few[32], sums[8 * kWarps];
+  uint64_t above_mass, out_place;
+  uint32_t above_cnt, bin_cnt, nlist, nfew;
   int bin;
   uint64_t total, before;
   int owner;
 };
 
-template <typename T, int THREADS, int NB, bool RES>
+template <typename T, int THREADS, bool RES>
 struct Sampler {
-  using S = SmShared<THREADS, NB>;
+  using S = SmShared<THREADS>;
   using V = SmVec<T>;
   static constexpr int W = THREADS / 32;
+  static constexpr int kList = sizeof(S::list) / 8;
   S& s;
   cg::cluster_group cluster;
   int C, rank;
-  const T* row;                             // the whole row
-  const uint4* data;                        // RES: the slice in shared memory, 16-byte vectors
+  const T* src;                             // the slice
+  const uint4* data;                        // its 16-byte vectors: in shared memory, or in place
   int first, len, phase;                    // slice: first index, length, unused leading values
   int nvec, vpw;                            // vectors of the slice, vectors a warp
   int lane, warp;
@@ -159,76 +213,106 @@ struct Sampler {
     return C == 1 ? p : cluster.map_shared_rank(p, q);
   }
 
-  // Vector v of the slice; values outside the row are -inf.
-  __device__ __forceinline__ void load(int v, float (&x)[V::N]) const {
-    if constexpr (RES) {
-      V::get(data[v], x);
-    } else {
+  // The first and the last vector of the slice hold values outside it, which read as -inf: they
+  // are put together once (one thread each).
+  __device__ __forceinline__ void make_ends() {
+    if (threadIdx.x < 2 && nvec > 0) {
+      const int v = threadIdx.x ? nvec - 1 : 0;
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = V::kMinusInf;
 #pragma unroll
       for (int j = 0; j < V::N; ++j) {
-        const int e = v * V::N + j;
-        x[j] = e < len ? sm_ld(row + first + e) : -CUDART_INF_F;
+        const int i = v * V::N + j - phase;
+        if (i >= 0 && i < len) V::put(w, j, src[i]);
       }
+      s.ends[threadIdx.x] = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    __syncthreads();
   }
-  __device__ __forceinline__ uint32_t index(int v, int j) const {
-    return (uint32_t)(first + v * V::N + j - phase);
+  // Vector v of the slice from memory.
+  __device__ __forceinline__ uint4 fetch(const uint4* g, int v) const {
+    const bool inner = (unsigned)(v - 1) < (unsigned)(nvec - 2);
+    const uint4* p = inner ? g + v : &s.ends[v > 0];
+    return *p;
   }
-  // f(value, index) for every value of the slice, each warp its own contiguous part.
+  __device__ __forceinline__ uint4 raw(int v) const { return RES ? data[v] : fetch(data, v); }
+  // Index of the first value of group g of vector v.
+  __device__ __forceinline__ uint32_t index(int v, int g) const {
+    return (uint32_t)(first + v * V::N + 4 * g - phase);
+  }
+  // f(four values, index of the first) for the groups of the slice that hold a value of at least
+  // `from`, each warp its own contiguous part.
   template <typename F>
-  __device__ __forceinline__ void each(F f) {
+  __device__ __forceinline__ void each(float from, F f) {
+    constexpr int U = RES ? 1 : 4;          // loads in flight
     const int v1 = min(nvec, (warp + 1) * vpw);
-    for (int v = warp * vpw + lane; v < v1; v += 32) {
-      float x[V::N];
-      load(v, x);
+    for (int v = warp * vpw + lane; v < v1; v += 32 * U) {
+      uint4 q[U];
 #pragma unroll
-      for (int j = 0; j < V::N; ++j) f(x[j], index(v, j));
+      for (int i = 0; i < U; ++i)
+        q[i] = raw(min(v + 32 * i, v1 - 1));
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int g = 0; g < V::N / 4; ++g) {
+          float x[4];
+          V::get(q[i], g, x);
+          if (fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= from && (i == 0 || v + 32 * i < v1))
+            f(x, index(v + 32 * i, g));
+        }
     }
+  }
+  // The weights of four logits (of which those that count are in [least, top]) and their bins.
+  __device__ __forceinline__ void weights(const float (&x)[4], uint64_t (&w)[4], int (&bin)[4]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = sm_weight(x[j], r, s.table, bin[j]);
   }
 
   __device__ __forceinline__ void clear() {
-    for (int b = threadIdx.x; b < NB; b += THREADS) s.lo[b] = s.hi[b] = s.cnt[b] = 0u;
+    for (int b = threadIdx.x; b < kSmBins; b += THREADS) s.h.lo[b] = s.h.hi[b] = s.h.cnt[b] = 0u;
     __syncthreads();
   }
-  __device__ __forceinline__ void add(int b, float x, bool mass, bool count) {
-    if (count) atomicAdd(&s.cnt[b], 1u);
-    if (mass) {
-      const uint64_t w = sm_weight(x, r);
-      const uint32_t l = (uint32_t)w, old = atomicAdd(&s.lo[b], l);
-      const uint32_t h = (uint32_t)(w >> 32) + (old + l < old ? 1u : 0u);
-      if (h) atomicAdd(&s.hi[b], h);
-    }
+  // lo, hi: the two words of a 64-bit sum
+  static __device__ __forceinline__ void add(uint32_t* lo, uint32_t* hi, uint64_t w) {
+    const uint32_t l = (uint32_t)w, old = atomicAdd(lo, l);
+    const uint32_t h = (uint32_t)(w >> 32) + (old + l < old ? 1u : 0u);
+    if (h) atomicAdd(hi, h);
   }
   // The cluster's histogram in every CTA.
-  __device__ void exchange(uint64_t* m, uint32_t* c) {
+  __device__ void exchange(bool mass, bool count) {
     sync();
-    const int seg = NB / C;
+    if (threadIdx.x == 0) s.nlist = s.nfew = 0u;
+    const int seg = kSmBins / C;
     for (int i = threadIdx.x; i < seg; i += THREADS) {
       const int b = rank * seg + i;
-      uint64_t mass = 0;
-      uint32_t count = 0;
-      for (int q = 0; q < C; ++q) {
-        mass += (uint64_t)*at(&s.hi[b], q) << 32;
-        mass += *at(&s.lo[b], q);
-        count += *at(&s.cnt[b], q);
+      uint32_t lo[8], hi[8], n[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {         // all reads in flight together
+        lo[q] = q < C && mass ? *at(&s.h.lo[b], q) : 0u;
+        hi[q] = q < C && mass ? *at(&s.h.hi[b], q) : 0u;
+        n[q] = q < C && count ? *at(&s.h.cnt[b], q) : 0u;
       }
-      for (int q = 0; q < C; ++q) {
-        *at(&m[b], q) = mass;
-        *at(&c[b], q) = count;
-      }
+      uint64_t m = 0;
+      uint32_t c = 0;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) m += ((uint64_t)hi[q] << 32) + lo[q], c += n[q];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < C) *at(&s.m0[b], q) = m, *at(&s.c0[b], q) = c;
     }
     sync();
   }
-  // First bin at which the running number reaches k, or the running mass reaches need; the sums
-  // before it go on top of above_mass / above_cnt.
-  __device__ void pick(const uint64_t* m, const uint32_t* c, bool by_count, uint32_t k, double need,
-                       uint64_t above_mass, uint32_t above_cnt) {
-    constexpr int PER = NB / THREADS;
+  // First bin at which the running number reaches k, or the running mass reaches need (s.bin,
+  // kSmBins if none does), what is before it and how many tokens it holds.
+  __device__ void pick(bool by_count, uint32_t k, double need, uint64_t above_mass, uint32_t above_cnt) {
+    constexpr int PER = (kSmBins + THREADS - 1) / THREADS;
     uint64_t mass[PER], msum = 0;
     uint32_t cnt[PER], csum = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      mass[i] = m[threadIdx.x * PER + i], cnt[i] = c[threadIdx.x * PER + i];
+      const int b = threadIdx.x * PER + i;
+      mass[i] = b < kSmBins ? s.m0[b] : 0ull, cnt[i] = b < kSmBins ? s.c0[b] : 0u;
       msum += mass[i], csum += cnt[i];
     }
     uint64_t mi = msum;
@@ -242,10 +326,16 @@ struct Sampler {
     const uint64_t mw = __shfl_sync(0xffffffffu, mi, 31);
     const uint32_t cw = __shfl_sync(0xffffffffu, ci, 31);
     if (lane == 0) s.wmass[warp] = mw, s.wcnt[warp] = cw;
-    if (threadIdx.x == 0) s.bin = NB - 1, s.bin_cnt = 0, s.above_mass = above_mass, s.above_cnt = above_cnt;
+    if (threadIdx.x == 0) s.bin = kSmBins;
     __syncthreads();
-    for (int q = 0; q < W; ++q)
-      if (q < warp) mi += s.wmass[q], ci += s.wcnt[q];
+    uint64_t before = lane < warp ? s.wmass[lane] : 0ull;      // (W <= 32)
+    uint32_t cbefore = lane < warp ? s.wcnt[lane] : 0u;
+#pragma unroll
+    for (int o = 1; o < W; o <<= 1) {
+      before += __shfl_xor_sync(0xffffffffu, before, o);
+      cbefore += __shfl_xor_sync(0xffffffffu, cbefore, o);
+    }
+    mi += __shfl_sync(0xffffffffu, before, 0), ci += __shfl_sync(0xffffffffu, cbefore, 0);
     uint64_t run_m = above_mass + mi - msum;
     uint32_t run_c = above_cnt + ci - csum;
 #pragma unroll
@@ -253,8 +343,7 @@ struct Sampler {
       const bool was = by_count ? run_c >= k : (double)run_m >= need;
       const uint64_t nm = run_m + mass[i];
       const uint32_t nc = run_c + cnt[i];
-      const bool is = by_count ? nc >= k : (double)nm >= need;
-      if (!was && is) {
+      if (!was && (by_count ? nc >= k : (double)nm >= need)) {
         s.bin = threadIdx.x * PER + i;
         s.bin_cnt = cnt[i];
         s.above_mass = run_m;
@@ -265,80 +354,118 @@ struct Sampler {
     __syncthreads();
   }
 
-  // The place of the last token that the truncation keeps and the mass through it.  Level 0's
-  // histogram (m0, c0) is there.
-  __device__ void find(bool by_count, uint32_t k, double need, bool mass, uint64_t whole,
-                       uint64_t* place, uint64_t* through) {
-    pick(s.m0, s.c0, by_count, k, need, 0ull, 0u);
-    int bin = s.bin;
-    if (bin == NB - 1) {                    // all of any weight is kept
-      *place = kSmAll, *through = whole;
-      __syncthreads();
-      return;
-    }
-    uint64_t above = s.above_mass;
-    uint32_t above_cnt = s.above_cnt, n = s.bin_cnt;
-    uint64_t lo = 0, hi = 0;
-    const int bin0 = bin;
-    for (int level = 0;; ++level) {
-      auto member = [&](float x, uint32_t i) {
-        if (level == 0) return sm_bin<NB>(x, r) == bin0;
-        const uint64_t c = sm_place(x, i);
-        return c >= lo && c <= hi;
-      };
-      if (n <= (uint32_t)S::kCap) {
-        // few: collect them in CTA 0, rank them, add their weights in order
-        if (threadIdx.x == 0) s.nlist = 0;
-        sync();
-        each([&](float x, uint32_t i) {
-          if (member(x, i)) {
-            const uint32_t j = atomicAdd(at(&s.nlist, 0), 1u);
-            if (j < (uint32_t)S::kCap) *at(&s.list[j], 0) = sm_place(x, i);
-          }
-        });
-        sync();
-        if (rank == 0) {
-          const int t = threadIdx.x;
-          uint64_t mine = kSmAll;
-          int at_rank = 0;
-          if (t < (int)n) {
-            mine = s.list[t];
-            for (uint32_t j = 0; j < n; ++j) at_rank += s.list[j] < mine;
-          }
-          __syncthreads();
-          if (t < (int)n) s.list[at_rank] = mine;
-          __syncthreads();
-          mine = t < (int)n ? s.list[t] : kSmAll;
-          const uint64_t w = mass && t < (int)n ? sm_weight(sm_place_value(mine), r) : 0ull;
-          uint64_t run = w;
+  // CTA 0: among the n places of the list, the one at which the running number reaches k, or the
+  // running mass reaches need, in ascending order; tells every CTA.  Histograms over places (in
+  // m0, c0) narrow the list down to at most 32 of them, which one warp ranks.
+  __device__ void resolve(uint32_t n, bool by_count, uint32_t k, double need, uint64_t above,
+                          uint32_t above_cnt) {
+    const uint32_t all = n;
+    uint64_t lo = 0, hi = kSmAll;
+    if (n > 32) {
+      lo = kSmAll, hi = 0;
+      for (uint32_t i = threadIdx.x; i < all; i += THREADS) lo = min(lo, s.list[i]), hi = max(hi, s.list[i]);
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const uint64_t a = __shfl_up_sync(0xffffffffu, run, o);
-            if (lane >= o) run += a;
-          }
-          const uint64_t ws = __shfl_sync(0xffffffffu, run, 31);
-          if (lane == 0) s.wmass[warp] = ws;
-          __syncthreads();
-          for (int q = 0; q < W; ++q)
-            if (q < warp) run += s.wmass[q];
-          run += above;
-          if (t < (int)n) {
-            const bool is = by_count ? above_cnt + t + 1 == k : (double)run >= need;
-            const bool was = !by_count && (double)(run - w) >= need;
-            if (is && !was)
-              for (int q = 0; q < C; ++q) *at(&s.out_place, q) = mine, *at(&s.out_mass, q) = run;
+      for (int o = 16; o > 0; o >>= 1) {
+        lo = min(lo, (uint64_t)__shfl_xor_sync(0xffffffffu, lo, o));
+        hi = max(hi, (uint64_t)__shfl_xor_sync(0xffffffffu, hi, o));
+      }
+      if (lane == 0) s.wsum[warp] = lo, s.wmass[warp] = hi;
+      __syncthreads();
+      lo = s.wsum[lane % W], hi = s.wmass[lane % W];
+#pragma unroll
+      for (int o = 1; o < W; o <<= 1) {
+        lo = min(lo, (uint64_t)__shfl_xor_sync(0xffffffffu, lo, o));
+        hi = max(hi, (uint64_t)__shfl_xor_sync(0xffffffffu, hi, o));
+      }
+    }
+    while (n > 32) {
+      const int shift = max(0, 64 - __clzll((long long)(hi - lo)) - 10);   // at most 1024 parts
+      for (int b = threadIdx.x; b < kSmBins; b += THREADS) s.m0[b] = 0ull, s.c0[b] = 0u;
+      __syncthreads();
+      for (uint32_t i = threadIdx.x; i < all; i += THREADS) {
+        const uint64_t c = s.list[i];
+        if (c >= lo && c <= hi) {
+          const int b = (int)((c - lo) >> shift);
+          int bin;
+          atomicAdd(&s.c0[b], 1u);
+          uint32_t* m = reinterpret_cast<uint32_t*>(&s.m0[b]);
+          if (!by_count) add(m, m + 1, sm_weight(sm_place_value(c), r, s.table, bin));
+        }
+      }
+      __syncthreads();
+      pick(by_count, k, need, above, above_cnt);
+      n = s.bin_cnt, above = s.above_mass, above_cnt = s.above_cnt;
+      lo += (uint64_t)s.bin << shift;
+      hi = lo + min(hi - lo, (uint64_t)((1ull << shift) - 1));
+      __syncthreads();
+    }
+    for (uint32_t i = threadIdx.x; i < all; i += THREADS) {
+      const uint64_t c = s.list[i];
+      if (c >= lo && c <= hi) s.few[atomicAdd(&s.nfew, 1u)] = c;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const uint64_t mine = lane < (int)n ? s.few[lane] : kSmAll;
+      int bin;
+      const uint64_t w = by_count || lane >= (int)n ? 0ull : sm_weight(sm_place_value(mine), r, s.table, bin);
+      uint64_t before = above;
+      uint32_t rank_of = above_cnt;
+      for (int j = 0; j < (int)n; ++j) {
+        const uint64_t c = __shfl_sync(0xffffffffu, mine, j), v = __shfl_sync(0xffffffffu, w, j);
+        if (c < mine) before += v, ++rank_of;
+      }
+      const bool is = by_count ? rank_of + 1 == k : (double)before < need && (double)(before + w) >= need;
+      if (is && lane < (int)n)
+        for (int q = 0; q < C; ++q) *at(&s.out_place, q) = mine;
+    }
+  }
+
+  // The place of the last token that a truncation keeps: the k-th (by_count), or that at which the
+  // running mass reaches need.  The cluster's histogram over bins is there; `from`: tokens below
+  // are not in it.
+  __device__ uint64_t find(bool by_count, uint32_t k, double need, float from, uint64_t limit) {
+    pick(by_count, k, need, 0ull, 0u);
+    if (s.bin == kSmBins) return limit;     // all that weighs anything is kept
+    const int bin0 = s.bin;
+    uint64_t above = s.above_mass;
+    uint32_t above_cnt = s.above_cnt;
+    // logits of the bin, a few roundings wider; which of them are in it is asked one by one
+    const double unit = 1.0 / r.c, x0 = r.topd + (-bin0 - 0.5) * unit, x1 = x0 + unit;
+    const double slack = 1e-6 * (fabs(r.topd) + fabs(x0) + unit);
+    const float low = fmaxf(from, __double2float_rd(x0 - slack)), high = __double2float_ru(x1 + slack);
+    uint64_t lo = 0, hi = kSmAll;
+    for (int level = 0;; ++level) {
+      auto member = [&](float x, uint32_t i, uint64_t& c) {
+        if (x > high || sm_bin(x, r) != bin0) return false;
+        c = sm_place(x, i);
+        return c >= lo && c <= hi && c <= limit;
+      };
+      // collect them in CTA 0 (the counters are 0 since the exchange); if they are too many for its
+      // list, split them first
+      each(low, [&](const float (&x)[4], uint32_t i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint64_t c;
+          if (x[e] >= low && member(x[e], i + e, c)) {
+            const uint32_t j = atomicAdd(at(&s.nlist, 0), 1u);
+            if (j < (uint32_t)kList) *at(&s.list[j], 0) = c;
           }
         }
+      });
+      sync();
+      const uint32_t n = *at(&s.nlist, 0);
+      if (n <= (uint32_t)kList) {
+        if (rank == 0) resolve(n, by_count, k, need, above, above_cnt);
         sync();
-        *place = s.out_place, *through = s.out_mass;
-        return;
+        return s.out_place;
       }
       if (level == 0) {                     // the range of places in the bin
         uint64_t a = kSmAll, b = 0;
-        each([&](float x, uint32_t i) {
-          if (sm_bin<NB>(x, r) == bin0) {
-            const uint64_t c = sm_place(x, i);
-            a = min(a, c), b = max(b, c);
+        each(low, [&](const float (&x)[4], uint32_t i) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint64_t c;
+            if (x[e] >= low && member(x[e], i + e, c)) a = min(a, c), b = max(b, c);
           }
         });
 #pragma unroll
@@ -356,17 +483,24 @@ struct Sampler {
         lo = kSmAll, hi = 0;
         for (int q = 0; q < C; ++q) lo = min(lo, *at(&s.part_lo, q)), hi = max(hi, *at(&s.part_hi, q));
       }
-      int shift = 64 - __clzll((long long)(hi - lo)) - (31 - __clz(NB));
-      shift = max(shift, 0);
+      const int shift = max(0, 64 - __clzll((long long)(hi - lo)) - 10);   // at most 1024 parts
       clear();
-      each([&](float x, uint32_t i) {
-        if (level == 0 && sm_bin<NB>(x, r) != bin0) return;
-        const uint64_t c = sm_place(x, i);
-        if (c >= lo && c <= hi) add((int)((c - lo) >> shift), x, mass, true);
+      each(low, [&](const float (&x)[4], uint32_t i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint64_t c;
+          if (x[e] >= low && member(x[e], i + e, c)) {
+            const int b = (int)((c - lo) >> shift);
+            int bin;
+            if (by_count) atomicAdd(&s.h.cnt[b], 1u);
+            else add(&s.h.lo[b], &s.h.hi[b], sm_weight(x[e], r, s.table, bin));
+          }
+        }
       });
-      exchange(s.m1, s.c1);
-      pick(s.m1, s.c1, by_count, k, need, above, above_cnt);
-      bin = s.bin, n = s.bin_cnt, above = s.above_mass, above_cnt = s.above_cnt;
+      exchange(!by_count, by_count);
+      pick(by_count, k, need, above, above_cnt);
+      const int bin = s.bin;
+      above = s.above_mass, above_cnt = s.above_cnt;
       lo += (uint64_t)bin << shift;
       hi = lo + min(hi - lo, (uint64_t)((1ull << shift) - 1));
       __syncthreads();
@@ -387,25 +521,23 @@ struct SmArgs {
   int slice;                                // values a CTA takes
 };
 
-template <typename T, int THREADS, int NB, bool RES>
-__global__ void __launch_bounds__(THREADS) sample_kernel(const SmArgs a) {
-  using Sm = Sampler<T, THREADS, NB, RES>;
+template <typename T, int THREADS, bool RES>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const SmArgs a) {
+  using Sm = Sampler<T, THREADS, RES>;
   using Vv = SmVec<T>;
   extern __shared__ __align__(16) unsigned char smem[];
-  SmShared<THREADS, NB>& s = *reinterpret_cast<SmShared<THREADS, NB>*>(smem);
-  constexpr size_t kData = (sizeof(SmShared<THREADS, NB>) + 15) / 16 * 16;
+  SmShared<THREADS>& s = *reinterpret_cast<SmShared<THREADS>*>(smem);
+  constexpr size_t kData = (sizeof(SmShared<THREADS>) + 15) / 16 * 16;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int64_t rw = blockIdx.x / C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const T* row = static_cast<const T*>(a.logits) + rw * a.ld;
-  const float t = a.temperature ? a.temperature[rw] : 1.f;
+  float t = a.temperature ? a.temperature[rw] : 1.f;
   const float p = a.top_p ? a.top_p[rw] : 1.f;
   const float mp = a.min_p ? a.min_p[rw] : 0.f;
   const double un = a.u[rw];
   const int k = a.top_k ? a.top_k[rw] : 0;
-  const bool bad = !(t >= 0.f && t < CUDART_INF_F && p > 0.f && p <= 1.f && mp >= 0.f && mp <= 1.f &&
-                     un >= 0.0 && un < 1.0);
+  const bool bad = !sm_valid(t, p, mp, un);
   if (bad) {
     if (rank == 0 && tid == 0) {
       a.ids[rw] = -1;
@@ -413,189 +545,179 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SmArgs a) {
     }
     return;
   }
+  // no CTA writes to another's memory before that one runs: arrive now, wait before the first write
+  if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (t > 0.f) t = fmaxf(t, kSmColdest);
+  if (tid < 32) s.table[tid] = exp2(40.0 + tid / 32.0);
   const int first = min(rank * a.slice, a.V), len = min(a.slice, a.V - first);
-  const T* src = row + first;
+  const T* src = static_cast<const T*>(a.logits) + rw * a.ld + first;
+  const int phase = (int)((uintptr_t)src % 16 / sizeof(T));
+  const uint4* g = reinterpret_cast<const uint4*>(src - phase);
   uint4* data = reinterpret_cast<uint4*>(smem + kData);
-  const int phase = RES ? (int)((uintptr_t)src % 16 / sizeof(T)) : 0;
   const int nvec = len > 0 ? (phase + len + Vv::N - 1) / Vv::N : 0;
-  Sm z = {s, cluster, C, rank, row, data, first, len, phase, nvec, (nvec + Sm::W - 1) / Sm::W,
-          lane, warp, {}};
+  Sm z = {s, cluster, C, rank, src, RES ? data : g, first, len, phase, nvec,
+          (nvec + Sm::W - 1) / Sm::W, lane, warp, {}};
 
-  // the slice to shared memory, and its maximum (NaN when it holds one)
+  z.make_ends();
+  // the maximum (NaN when there is one); RES: the slice goes to shared memory
   float best = -CUDART_INF_F;
-  if constexpr (RES) {
-    const uint4* g = reinterpret_cast<const uint4*>(src - phase);
-    for (int v0 = tid; v0 < nvec; v0 += THREADS * 8) {
-      uint4 q[8];
+  for (int v0 = tid; v0 < nvec; v0 += THREADS * 8) {
+    uint4 q[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int v = v0 + i * THREADS;
-        if (v < nvec) {
-          if (v * Vv::N >= phase && (v + 1) * Vv::N <= phase + len) {
-            q[i] = __ldcs(g + v);
-          } else {                          // the ragged ends of the slice
-            T e[Vv::N];
-            uint4 w = make_uint4(Vv::kMinusInf, Vv::kMinusInf, Vv::kMinusInf, Vv::kMinusInf);
-            memcpy(e, &w, 16);
+    for (int i = 0; i < 8; ++i)
+      if (v0 + i * THREADS < nvec) q[i] = z.fetch(g, v0 + i * THREADS);
 #pragma unroll
-            for (int j = 0; j < Vv::N; ++j) {
-              const int at = v * Vv::N + j - phase;
-              if (at >= 0 && at < len) e[j] = src[at];
-            }
-            memcpy(&w, e, 16);
-            q[i] = w;
-          }
+    for (int i = 0; i < 8; ++i) {
+      const int v = v0 + i * THREADS;
+      if (v < nvec) {
+#pragma unroll
+        for (int g = 0; g < Vv::N / 4; ++g) {
+          float x[4];
+          Vv::get(q[i], g, x);
+          best = sm_max_nan(best, sm_max_nan(sm_max_nan(x[0], x[1]), sm_max_nan(x[2], x[3])));
         }
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int v = v0 + i * THREADS;
-        if (v < nvec) {
-          float x[Vv::N];
-          Vv::get(q[i], x);
-#pragma unroll
-          for (int j = 0; j < Vv::N; ++j) best = sm_max_nan(best, x[j]);
-          data[v] = q[i];
-        }
+        if (RES) data[v] = q[i];
       }
     }
-  } else {
-    z.each([&](float x, uint32_t) { best = sm_max_nan(best, x); });
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) best = sm_max_nan(best, __shfl_xor_sync(0xffffffffu, best, o));
   if (lane == 0) s.wmax[warp] = best;
+  if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   __syncthreads();
   if (tid == 0) {
     for (int q = 0; q < Sm::W; ++q) best = sm_max_nan(best, s.wmax[q]);
-    s.part_max = best;
+    for (int q = 0; q < C; ++q) *z.at(&s.part_max[rank], q) = best;
   }
   z.sync();
-  float top = -CUDART_INF_F;
-  for (int q = 0; q < C; ++q) top = sm_max_nan(top, *z.at(&s.part_max, q));
+  float top = s.part_max[0];
+  for (int q = 1; q < C; ++q) top = sm_max_nan(top, s.part_max[q]);
   if (isnan(top) || top == -CUDART_INF_F) {
     if (rank == 0 && tid == 0) {
       a.ids[rw] = -1;
       if (a.prob) a.prob[rw] = isnan(top) ? CUDART_NAN_F : 0.f;
     }
-    z.sync();                               // the others may still read this CTA's maximum
     return;
   }
-  z.r.top = top;
-  z.r.half_top = 0.5f * top;
-  z.r.bin_scale = 2.f * (NB - 1) / 28.5f / t;
-  z.r.topd = (double)top;
-  z.r.c = t > 0.f ? 1.4426950408889634 / (double)t : 0.0;
+  z.r = sm_row(top, t);
   const SmRow r = z.r;
 
   // the border: place of the last kept token
   uint64_t border = kSmAll;
+  float from = r.least;                     // the border's logit, or the least that weighs anything
   if (t == 0.f) {
+    from = top;
     border = sm_place(top, 0xffffffffu);
   } else {
-    const bool by_k = k > 0 && k < a.V, by_p = p < 1.f;
-    if (by_k || by_p) {
+    if (k > 0 && k < a.V) {
       z.clear();
-      z.each([&](float x, uint32_t) {
-        const int b = sm_bin<NB>(x, r);
-        if (b < NB - 1) z.add(b, x, by_p, by_k || by_p);
-      });
-      z.exchange(s.m0, s.c0);
-      uint64_t whole = 0;
-      if (by_p) {
-        uint64_t m = 0;
-        for (int b = tid; b < NB; b += THREADS) m += s.m0[b];
+      z.each(from, [&](const float (&x)[4], uint32_t) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-        if (lane == 0) s.wsum[warp] = m;
-        __syncthreads();
-        for (int q = 0; q < Sm::W; ++q) whole += s.wsum[q];
-        __syncthreads();
-      }
-      if (by_k) z.find(true, (uint32_t)k, 0.0, by_p, whole, &border, &whole);
-      if (by_p) {
-        uint64_t through;
-        z.find(false, 0u, (double)p * (double)whole, true, whole, &border, &through);
-      }
+        for (int e = 0; e < 4; ++e)
+          if (x[e] >= from) atomicAdd(&s.h.cnt[sm_bin(x[e], r)], 1u);
+      });
+      z.exchange(false, true);
+      border = z.find(true, (uint32_t)k, 0.0, from, border);
+      if (border != kSmAll) from = fmaxf(from, sm_place_value(border));
+    }
+    if (p < 1.f) {
+      z.clear();
+      const uint32_t il = (uint32_t)border;
+      z.each(from, [&](const float (&x)[4], uint32_t i) {
+        uint64_t w[4];
+        int bin[4];
+        z.weights(x, w, bin);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (x[e] > from || (x[e] == from && i + e <= il)) z.add(&s.h.lo[bin[e]], &s.h.hi[bin[e]], w[e]);
+      });
+      z.exchange(true, false);
+      uint64_t whole = 0, m = 0;
+      for (int b = tid; b < kSmBins; b += THREADS) m += s.m0[b];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+      if (lane == 0) s.wsum[warp] = m;
+      __syncthreads();
+      for (int q = 0; q < Sm::W; ++q) whole += s.wsum[q];
+      __syncthreads();
+      border = z.find(false, 0u, (double)p * (double)whole, from, border);
+      if (border != kSmAll) from = fmaxf(from, sm_place_value(border));
     }
     if (mp > 0.f) {
-      // the smallest logit with (x - top) / T >= log(min_p): bisection over keys, at first round
-      // the nearest float to top + T log(min_p)
-      const double cut = log((double)mp) * 1.4426950408889634;
-      auto in = [&](uint32_t key) {
-        const float x = sm_value(key);
-        return x == top || ((double)x - (double)top) * r.c >= cut;
-      };
-      const uint32_t lowest = 0x007fffffu, top_key = sm_key(top);   // key of -inf: never in
-      const uint32_t guess = sm_key((float)fmax((double)top + cut / r.c, -3.4e38));
-      uint32_t lo = guess > lowest + 4 && !in(guess - 4) ? guess - 4 : lowest;
-      uint32_t hi = guess < top_key - 4 && in(guess + 4) ? guess + 4 : top_key;
-      while (hi - lo > 1) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        if (in(mid)) hi = mid;
-        else lo = mid;
-      }
-      border = min(border, (uint64_t)(~hi) << 32 | 0xffffffffu);
+      border = min(border, sm_min_p(mp, r));
+      from = fmaxf(from, sm_place_value(border));
     }
   }
-  const float xb = border == kSmAll ? -CUDART_INF_F : sm_place_value(border);
-  const uint32_t ib = (uint32_t)border;
-  auto weight = [&](float x, uint32_t i) -> uint64_t {
-    if (x > xb || (x == xb && i <= ib)) {
-      if (sm_bin<NB>(x, r) < NB - 1) return sm_weight(x, r);
+  // tokens above `from` count, and those at it up to index ib
+  const uint32_t ib = border == kSmAll || sm_place_value(border) < from ? 0xffffffffu : (uint32_t)border;
+  auto kept = [&](const float (&x)[4], uint32_t i, uint64_t (&w)[4]) {
+    int bin[4];
+    if (t == 0.f) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = 1ull;
+    } else {
+      z.weights(x, w, bin);
     }
-    return 0ull;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = x[e] > from || (x[e] == from && i + e <= ib) ? w[e] : 0ull;
   };
   uint64_t mass = 0;
-  z.each([&](float x, uint32_t i) { mass += weight(x, i); });
+  z.each(from, [&](const float (&x)[4], uint32_t i) {
+    uint64_t w[4];
+    kept(x, i, w);
+    mass += (w[0] + w[1]) + (w[2] + w[3]);
+  });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
-  if (lane == 0) s.wsum[warp] = mass;
-  z.sync();
+  if (lane < C) *z.at(&s.sums[rank * Sm::W + warp], lane) = mass;
+  z.sync();                                 // the last access to another CTA's memory is before this
   // the warp whose part holds the target
   if (tid < 32) {
-    uint64_t total = 0;
-    const int n = C * Sm::W;
-    for (int q0 = 0; q0 < n; q0 += 32) {
-      const int q = q0 + lane;
-      uint64_t w = q < n ? *z.at(&s.wsum[q % Sm::W], q / Sm::W) : 0ull;
+    constexpr int PER = Sm::W * 8 / 32;     // sums a lane, in order
+    uint64_t w[PER], sum = 0;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-      total += w;
+    for (int i = 0; i < PER; ++i) {
+      const int q = lane * PER + i;
+      w[i] = q < C * Sm::W ? s.sums[q] : 0ull;
     }
-    const uint64_t target = t == 0.f ? 0ull : min((uint64_t)(un * (double)total), total - 1);
-    uint64_t run = 0;
-    for (int q0 = 0; q0 < n; q0 += 32) {
-      const int q = q0 + lane;
-      const uint64_t w = q < n ? *z.at(&s.wsum[q % Sm::W], q / Sm::W) : 0ull;
-      uint64_t inc = w;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t b = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += b;
-      }
-      const uint64_t end = run + inc, start = end - w;
-      if (w > 0 && end > target && start <= target) {
-        s.owner = q;
+    for (int i = 0; i < PER; ++i) sum += w[i];
+    uint64_t inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t b = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += b;
+    }
+    const uint64_t total = __shfl_sync(0xffffffffu, inc, 31);
+    const uint64_t target = t == 0.f ? 0ull : min((uint64_t)(un * (double)total), total - 1);
+    uint64_t start = inc - sum;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (start <= target && start + w[i] > target) {
+        s.owner = lane * PER + i;
         s.before = target - start;          // weight to pass inside the part
         s.total = total;
       }
-      run += __shfl_sync(0xffffffffu, inc, 31);
+      start += w[i];
     }
   }
   __syncthreads();
-  if (C > 1) cluster.sync();                // no CTA leaves while its sums may be read
   if (s.owner != rank * Sm::W + warp) return;
-  uint64_t target = s.before, run = 0;
+  const uint64_t target = s.before;
+  uint64_t run = 0;
   const int v1 = min(nvec, (warp + 1) * z.vpw);
   for (int v0 = warp * z.vpw; v0 < v1; v0 += 32) {
     const int v = v0 + lane;
-    float x[Vv::N];
-    uint64_t w[Vv::N], sum = 0;
-    if (v < v1) {
-      z.load(v, x);
+    constexpr int G = Vv::N / 4;
+    uint4 q = make_uint4(0u, 0u, 0u, 0u);
+    uint64_t w[G][4], sum = 0;
+    if (v < v1) q = z.raw(v);
 #pragma unroll
-      for (int j = 0; j < Vv::N; ++j) w[j] = weight(x[j], z.index(v, j)), sum += w[j];
+    for (int g = 0; g < G; ++g) {
+      float x[4];
+      Vv::get(q, g, x);
+      kept(x, z.index(v, g), w[g]);
+      sum += v < v1 ? (w[g][0] + w[g][1]) + (w[g][2] + w[g][3]) : 0ull;
     }
     uint64_t inc = sum;
 #pragma unroll
@@ -604,17 +726,19 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SmArgs a) {
       if (lane >= o) inc += b;
     }
     uint64_t at = run + inc - sum;
-    if (sum > 0 && at <= target && at + sum > target) {
+    if (at <= target && at + sum > target) {
 #pragma unroll
-      for (int j = 0; j < Vv::N; ++j) {
-        if (at <= target && at + w[j] > target) {
-          a.ids[rw] = (int32_t)z.index(v, j);
-          if (a.prob)
-            a.prob[rw] = t == 0.f ? 1.f
-                         : (float)((x[j] == top ? 1.0 : exp(((double)x[j] - (double)top) / (double)t)) *
-                                   kSmOne / (double)s.total);
+      for (int g = 0; g < G; ++g) {
+        float x[4];
+        Vv::get(q, g, x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (at <= target && at + w[g][e] > target) {
+            a.ids[rw] = (int32_t)(z.index(v, g) + e);
+            if (a.prob) a.prob[rw] = sm_prob(x[e], top, t, s.total);
+          }
+          at += w[g][e];
         }
-        at += w[j];
       }
     }
     run += __shfl_sync(0xffffffffu, inc, 31);
@@ -622,9 +746,136 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SmArgs a) {
   }
 }
 
-template <typename T, int THREADS, int NB, bool RES>
+// One warp a row, for rows of at most kSmWarpV values without top-k and top-p: the row stays in
+// registers.  A CTA a row spends its time on barriers there.
+constexpr int kSmWarpV = 1024;
+
+template <typename T>
+__global__ void __launch_bounds__(256) sample_warp_kernel(const SmArgs a, int64_t rows) {
+  using Vv = SmVec<T>;
+  constexpr int G = Vv::N / 4, NS = kSmWarpV / Vv::N / 32 + 1;   // groups a vector, vectors a lane
+  __shared__ double table[32];
+  const int lane = threadIdx.x & 31;
+  const int64_t rw = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (threadIdx.x < 32) table[threadIdx.x] = exp2(40.0 + threadIdx.x / 32.0);
+  __syncthreads();
+  if (rw >= rows) return;
+  float t = a.temperature ? a.temperature[rw] : 1.f;
+  const float mp = a.min_p ? a.min_p[rw] : 0.f;
+  const double un = a.u[rw];
+  const T* src = static_cast<const T*>(a.logits) + rw * a.ld;
+  const int phase = (int)((uintptr_t)src % 16 / sizeof(T)), nvec = (phase + a.V + Vv::N - 1) / Vv::N;
+  const uint4* g = reinterpret_cast<const uint4*>(src - phase);
+  uint4 q[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    const int v = lane + 32 * i;
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = Vv::kMinusInf;
+    if (v * Vv::N >= phase && (v + 1) * Vv::N <= phase + a.V) {
+      q[i] = __ldg(g + v);
+    } else {
+      if (v < nvec) {                       // the ragged ends of the row
+#pragma unroll
+        for (int j = 0; j < Vv::N; ++j) {
+          const int e = v * Vv::N + j - phase;
+          if (e >= 0 && e < a.V) Vv::put(w, j, src[e]);
+        }
+      }
+      q[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  float top = -CUDART_INF_F;
+#pragma unroll
+  for (int i = 0; i < NS; ++i)
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+      float x[4];
+      Vv::get(q[i], h, x);
+      top = sm_max_nan(top, sm_max_nan(sm_max_nan(x[0], x[1]), sm_max_nan(x[2], x[3])));
+    }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = sm_max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const bool bad = !sm_valid(t, 1.f, mp, un) || isnan(top);
+  if (bad || top == -CUDART_INF_F) {
+    if (lane == 0) {
+      a.ids[rw] = -1;
+      if (a.prob) a.prob[rw] = bad ? CUDART_NAN_F : 0.f;
+    }
+    return;
+  }
+  if (t > 0.f) t = fmaxf(t, kSmColdest);
+  const SmRow r = sm_row(top, t);
+  float from = r.least;
+  if (t == 0.f) from = top;
+  else if (mp > 0.f) from = fmaxf(from, sm_place_value(sm_min_p(mp, r)));
+  auto weight = [&](float x) -> uint64_t {
+    int bin;
+    return x >= from ? (t == 0.f ? 1ull : sm_weight(x, r, table, bin)) : 0ull;
+  };
+  // per 32 vectors (they are contiguous), the warp's sum
+  uint64_t part[NS], total = 0;
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    part[i] = 0;
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+      float x[4];
+      Vv::get(q[i], h, x);
+      if (fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= from)
+        part[i] += (weight(x[0]) + weight(x[1])) + (weight(x[2]) + weight(x[3]));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) part[i] += __shfl_xor_sync(0xffffffffu, part[i], o);
+    total += part[i];
+  }
+  const uint64_t target = t == 0.f ? 0ull : min((uint64_t)(un * (double)total), total - 1);
+  uint64_t run = 0;
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    if (run <= target && run + part[i] > target) {
+      uint64_t w[Vv::N], sum = 0;
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        float x[4];
+        Vv::get(q[i], h, x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum += w[4 * h + e] = weight(x[e]);
+      }
+      uint64_t inc = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t b = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += b;
+      }
+      uint64_t at = run + inc - sum;
+      if (at <= target && at + sum > target) {
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          float x[4];
+          Vv::get(q[i], h, x);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (at <= target && at + w[4 * h + e] > target) {
+              a.ids[rw] = (lane + 32 * i) * Vv::N + 4 * h + e - phase;
+              if (a.prob) a.prob[rw] = sm_prob(x[e], top, t, total);
+            }
+            at += w[4 * h + e];
+          }
+        }
+      }
+    }
+    run += part[i];
+  }
+}
+
+template <typename T, int THREADS, bool RES>
 cudaError_t sm_launch(const SmArgs& a, int64_t rows, int C, size_t smem, cudaStream_t st) {
-  auto* k = sample_kernel<T, THREADS, NB, RES>;
+  auto* k = sample_kernel<T, THREADS, RES>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -647,23 +898,26 @@ cudaError_t sm_choose(SmArgs a, int64_t rows, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  constexpr int kSmall = 128, kSmallBins = 256, kLarge = 512, kBins = 1024;
-  constexpr size_t kFixedSmall = (sizeof(SmShared<kSmall, kSmallBins>) + 15) / 16 * 16;
-  constexpr size_t kFixed = (sizeof(SmShared<kLarge, kBins>) + 15) / 16 * 16;
-  constexpr size_t kHalf = 113 * 1024, kFull = 227 * 1024;   // two CTAs a SM, one CTA a SM
+  constexpr int kSmall = 128, kLarge = 512;
+  constexpr size_t kFixedSmall = (sizeof(SmShared<kSmall>) + 15) / 16 * 16;
+  constexpr size_t kFixed = (sizeof(SmShared<kLarge>) + 15) / 16 * 16;
+  constexpr size_t kHalf = 113 * 1024;      // two CTAs a SM
   const auto bytes = [&](int C) { return ((size_t)((a.V + C - 1) / C) * sizeof(T) + 31) / 16 * 16; };
+  if (a.V <= kSmWarpV && !a.top_k && !a.top_p) {
+    sample_warp_kernel<T><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(a, rows);
+    return cudaGetLastError();
+  }
   if (a.V <= 4096) {
     a.slice = a.V;
-    return sm_launch<T, kSmall, kSmallBins, true>(a, rows, 1, kFixedSmall + bytes(1), st);
+    return sm_launch<T, kSmall, true>(a, rows, 1, kFixedSmall + bytes(1), st);
   }
-  // as many CTAs a row as its slices need to lie two to a SM; more while the rows leave SMs idle
   int C = 1;
-  while (C < 8 && (kFixed + bytes(C) > kHalf || (rows * C < 2 * sms && a.V / C > 4096))) C *= 2;
+  while (C < 8 && rows * C < sms && a.V / C > 4096) C *= 2;
   a.slice = (a.V + C - 1) / C;
   if (rows * C > INT32_MAX) return cudaErrorInvalidValue;
-  if (kFixed + bytes(C) <= kFull)
-    return sm_launch<T, kLarge, kBins, true>(a, rows, C, kFixed + bytes(C), st);
-  return sm_launch<T, kLarge, kBins, false>(a, rows, C, kFixed, st);
+  if (kFixed + bytes(C) <= kHalf)
+    return sm_launch<T, kLarge, true>(a, rows, C, kFixed + bytes(C), st);
+  return sm_launch<T, kLarge, false>(a, rows, C, kFixed, st);
 }
 
 }  // namespace
