@@ -94,6 +94,17 @@ struct SmRow {
   double topd, c;                           // c = 32 log2(e) / T
 };
 
+// 2^(40 + j / 32)
+__device__ const double kSmTable[32] = {
+    1099511627776.0, 1123587797336.3408, 1148191166360.5662, 1173333279013.7073,
+    1199025932245.0925, 1225281181323.604, 1252111345494.1387, 1279529013757.9299,
+    1307547050779.4426, 1336178602922.6121, 1365437104419.2583, 1395336283672.5735,
+    1425890169698.6345, 1457113098708.9692, 1489019720837.26, 1521625007013.345,
+    1554944255987.7375, 1588993101509.9658, 1623787519664.0955, 1659343836364.8796,
+    1695678735018.0535, 1732809264348.3684, 1770752846399.0352, 1809527284706.3352,
+    1849150772653.2297, 1889641902005.8923, 1931019671637.1631, 1973303496441.0256,
+    2016513216442.283, 2060669106105.7107, 2105791883849.0532, 2151902721764.3281};
+
 constexpr double kSmMagic = 6755399441055744.0;  // 1.5 2^52: a sum's low word is the rounded integer
 constexpr float kSmColdest = 8.271806125530277e-25f;  // 2^-80: logits that differ by 2^-74 or more differ
                                             // in weight by more than 2^-42 at any lower temperature too
@@ -103,45 +114,41 @@ constexpr int kSmBins = 1344;               // 32 bins a factor of two, down to 
 __device__ __forceinline__ int sm_bin(float x, const SmRow& r) {
   return -__double2loint(fma(sm_double(x) - r.topd, r.c, kSmMagic));
 }
-// round(2^40 2^(y / 32)), y = (x - top) c in [-1322, 0]: y = n + f with |f| <= 1/2; 2^(f / 32) by its
-// Taylor series to f^5 (remainder 2^-48); table[j] = 2^(40 + j / 32), whose exponent takes n / 32;
-// the product is rounded by adding 2^52.  Ten fp64 operations.
-__device__ __forceinline__ uint64_t sm_weight(float x, const SmRow& r, const double* table, int& bin) {
+// 2^40 2^(y / 32), y = (x - top) c in [-1322, 0], and the bin -round(y).  y = n + f with |f| <= 1/2;
+// 2^(f / 32) by its Taylor series to f^5 (remainder 2^-48); table[j] = 2^(40 + j / 32), whose exponent
+// takes n / 32.  The result is p t, before its rounding.
+__device__ __forceinline__ void sm_exp(float x, const SmRow& r, const double* table, int& bin,
+                                       double& p, double& t) {
   const double d = sm_double(x) - r.topd;
   const double k = fma(d, r.c, kSmMagic);
   const double f = fma(d, r.c, kSmMagic - k);
-  double p = 3.97370998454941609e-11;       // (ln 2 / 32)^5 / 5!
+  p = 3.97370998454941609e-11;       // (ln 2 / 32)^5 / 5!
   p = fma(p, f, 9.17256270182464302e-09);
   p = fma(p, f, 1.69385097243718210e-06);
   p = fma(p, f, 2.34596198202246799e-04);
   p = fma(p, f, 2.16608493924982902e-02);
   p = fma(p, f, 1.0);
   const int n = __double2loint(k);
-  const double t = table[n & 31];
-  const double m = fma(p, __hiloint2double(__double2hiint(t) + (n >> 5) * (1 << 20), __double2loint(t)),
-                       4503599627370496.0);
+  t = table[n & 31];
+  t = __hiloint2double(__double2hiint(t) + (n >> 5) * (1 << 20), __double2loint(t));
   bin = -n;
+}
+// The weight of a logit, and its bin.
+__device__ __forceinline__ uint64_t sm_weight(float x, const SmRow& r, const double* table, int& bin) {
+  double p, t;
+  sm_exp(x, r, table, bin, p, t);
+  const double m = fma(p, t, 4503599627370496.0);   // 2^52: the mantissa holds the rounded product
   return (uint64_t)__double_as_longlong(m) & 0xfffffffffffffull;
 }
 
-// The last place that min-p keeps: that of the smallest logit with (x - top) / T >= log(min_p), by
-// bisection over keys, at first round the nearest float to top + T log(min_p).
-__device__ __forceinline__ uint64_t sm_min_p(float mp, const SmRow& r) {
-  const double cut = log((double)mp) * 46.166241308446828;
-  auto in = [&](uint32_t key) {
-    const float x = sm_value(key);
-    return x == r.top || ((double)x - (double)r.top) * r.c >= cut;
-  };
-  const uint32_t lowest = 0x007fffffu, top_key = sm_key(r.top);   // key of -inf: never in
-  const uint32_t guess = sm_key((float)fmax((double)r.top + cut / r.c, -3.4e38));
-  uint32_t lo = guess > lowest + 4 && !in(guess - 4) ? guess - 4 : lowest;
-  uint32_t hi = guess < top_key - 4 && in(guess + 4) ? guess + 4 : top_key;
-  while (hi - lo > 1) {
-    const uint32_t mid = lo + (hi - lo) / 2;
-    if (in(mid)) hi = mid;
-    else lo = mid;
-  }
-  return (uint64_t)(~hi) << 32 | 0xffffffffu;
+// min-p: the least weight it keeps, and a logit that is surely below every logit of that weight.
+__device__ __forceinline__ uint64_t sm_min_weight(float mp) {
+  return (uint64_t)__double2ull_ru((double)mp * kSmOne);
+}
+__device__ __forceinline__ float sm_min_logit(float mp, float t, const SmRow& r) {
+  // log2(mp) <= 0, a relative error of 2^-20 at most allowed for, and 2^-38 for the weights' rounding
+  const float down = fmaf(__log2f(mp), 0.6931482f * 1.00001f, -1e-5f) * t;
+  return __double2float_rd((double)r.top + (double)down * 1.00001 - 1e-5 * (double)t);
 }
 // Bounds of a row's parameters (NaN fails them).
 __device__ __forceinline__ bool sm_valid(float t, float p, float mp, double u) {
@@ -156,9 +163,13 @@ __device__ __forceinline__ SmRow sm_row(float top, float t) {
   r.least = fminf(__double2float_ru((double)top - 28.62 * (double)t), top);
   return r;
 }
-__device__ __forceinline__ float sm_prob(float x, float top, float t, uint64_t total) {
+__device__ __forceinline__ float sm_prob(float x, const SmRow& r, const double* table, float t,
+                                         uint64_t total) {
   if (t == 0.f) return 1.f;
-  return (float)((x == top ? 1.0 : exp(((double)x - (double)top) / (double)t)) * kSmOne / (double)total);
+  int bin;
+  double p, e;
+  sm_exp(x, r, table, bin, p, e);
+  return (float)(p * e / (double)total);
 }
 
 constexpr int kSmList = 2048;               // tokens of a border bin that are sorted
@@ -548,7 +559,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
   // no CTA writes to another's memory before that one runs: arrive now, wait before the first write
   if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   if (t > 0.f) t = fmaxf(t, kSmColdest);
-  if (tid < 32) s.table[tid] = exp2(40.0 + tid / 32.0);
+  if (tid < 32) s.table[tid] = kSmTable[tid];
   const int first = min(rank * a.slice, a.V), len = min(a.slice, a.V - first);
   const T* src = static_cast<const T*>(a.logits) + rw * a.ld + first;
   const int phase = (int)((uintptr_t)src % 16 / sizeof(T));
@@ -643,11 +654,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
       border = z.find(false, 0u, (double)p * (double)whole, from, border);
       if (border != kSmAll) from = fmaxf(from, sm_place_value(border));
     }
-    if (mp > 0.f) {
-      border = min(border, sm_min_p(mp, r));
-      from = fmaxf(from, sm_place_value(border));
-    }
+    if (mp > 0.f) from = fmaxf(from, sm_min_logit(mp, t, r));
   }
+  const uint64_t least = t > 0.f ? sm_min_weight(mp) : 0ull;   // weight that min-p asks for
   // tokens above `from` count, and those at it up to index ib
   const uint32_t ib = border == kSmAll || sm_place_value(border) < from ? 0xffffffffu : (uint32_t)border;
   auto kept = [&](const float (&x)[4], uint32_t i, uint64_t (&w)[4]) {
@@ -659,7 +668,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
       z.weights(x, w, bin);
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = x[e] > from || (x[e] == from && i + e <= ib) ? w[e] : 0ull;
+    for (int e = 0; e < 4; ++e)
+      w[e] = (x[e] > from || (x[e] == from && i + e <= ib)) && w[e] >= least ? w[e] : 0ull;
   };
   uint64_t mass = 0;
   z.each(from, [&](const float (&x)[4], uint32_t i) {
@@ -735,7 +745,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
         for (int e = 0; e < 4; ++e) {
           if (at <= target && at + w[g][e] > target) {
             a.ids[rw] = (int32_t)(z.index(v, g) + e);
-            if (a.prob) a.prob[rw] = sm_prob(x[e], top, t, s.total);
+            if (a.prob) a.prob[rw] = sm_prob(x[e], r, s.table, t, s.total);
           }
           at += w[g][e];
         }
@@ -746,18 +756,21 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
   }
 }
 
-// One warp a row, for rows of at most kSmWarpV values without top-k and top-p: the row stays in
-// registers.  A CTA a row spends its time on barriers there.
-constexpr int kSmWarpV = 1024;
+// One warp a row, for rows of at most kSmWarpV values without top-k and top-p: a CTA a row spends
+// its time on barriers there.  The row lies in shared memory, and loops are short: with the row in
+// registers and every loop unrolled, the warps waited for instructions.
+constexpr int kSmWarpV = 1024, kSmWarps = 4;
 
 template <typename T>
-__global__ void __launch_bounds__(256) sample_warp_kernel(const SmArgs a, int64_t rows) {
+__global__ void __launch_bounds__(32 * kSmWarps) sample_warp_kernel(const SmArgs a, int64_t rows) {
   using Vv = SmVec<T>;
-  constexpr int G = Vv::N / 4, NS = kSmWarpV / Vv::N / 32 + 1;   // groups a vector, vectors a lane
+  constexpr int G = Vv::N / 4, NV = kSmWarpV / Vv::N + 1;   // groups a vector, vectors a row
+  __shared__ uint4 data[kSmWarps][NV];
+  __shared__ uint16_t list[kSmWarps][kSmWarpV];
   __shared__ double table[32];
-  const int lane = threadIdx.x & 31;
-  const int64_t rw = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (threadIdx.x < 32) table[threadIdx.x] = exp2(40.0 + threadIdx.x / 32.0);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t rw = (int64_t)blockIdx.x * kSmWarps + warp;
+  if (threadIdx.x < 32) table[threadIdx.x] = kSmTable[threadIdx.x];
   __syncthreads();
   if (rw >= rows) return;
   float t = a.temperature ? a.temperature[rw] : 1.f;
@@ -766,35 +779,33 @@ __global__ void __launch_bounds__(256) sample_warp_kernel(const SmArgs a, int64_
   const T* src = static_cast<const T*>(a.logits) + rw * a.ld;
   const int phase = (int)((uintptr_t)src % 16 / sizeof(T)), nvec = (phase + a.V + Vv::N - 1) / Vv::N;
   const uint4* g = reinterpret_cast<const uint4*>(src - phase);
-  uint4 q[NS];
-#pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    const int v = lane + 32 * i;
+  uint4* row = data[warp];
+#pragma unroll 4
+  for (int v = lane; v < nvec; v += 32)
+    if (v * Vv::N >= phase && (v + 1) * Vv::N <= phase + a.V) row[v] = __ldg(g + v);
+  const int v0 = lane ? nvec - 1 : 0;       // the ragged ends of the row
+  if (lane < 2 && !(v0 * Vv::N >= phase && (v0 + 1) * Vv::N <= phase + a.V)) {
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[j] = Vv::kMinusInf;
-    if (v * Vv::N >= phase && (v + 1) * Vv::N <= phase + a.V) {
-      q[i] = __ldg(g + v);
-    } else {
-      if (v < nvec) {                       // the ragged ends of the row
 #pragma unroll
-        for (int j = 0; j < Vv::N; ++j) {
-          const int e = v * Vv::N + j - phase;
-          if (e >= 0 && e < a.V) Vv::put(w, j, src[e]);
-        }
-      }
-      q[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int j = 0; j < Vv::N; ++j) {
+      const int e = v0 * Vv::N + j - phase;
+      if (e >= 0 && e < a.V) Vv::put(w, j, src[e]);
     }
+    row[v0] = make_uint4(w[0], w[1], w[2], w[3]);
   }
+  __syncwarp();
   float top = -CUDART_INF_F;
-#pragma unroll
-  for (int i = 0; i < NS; ++i)
+  for (int v = lane; v < nvec; v += 32) {
+    const uint4 q = row[v];
 #pragma unroll
     for (int h = 0; h < G; ++h) {
       float x[4];
-      Vv::get(q[i], h, x);
+      Vv::get(q, h, x);
       top = sm_max_nan(top, sm_max_nan(sm_max_nan(x[0], x[1]), sm_max_nan(x[2], x[3])));
     }
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = sm_max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
   const bool bad = !sm_valid(t, 1.f, mp, un) || isnan(top);
@@ -809,67 +820,48 @@ __global__ void __launch_bounds__(256) sample_warp_kernel(const SmArgs a, int64_
   const SmRow r = sm_row(top, t);
   float from = r.least;
   if (t == 0.f) from = top;
-  else if (mp > 0.f) from = fmaxf(from, sm_place_value(sm_min_p(mp, r)));
-  auto weight = [&](float x) -> uint64_t {
+  else if (mp > 0.f) from = fmaxf(from, sm_min_logit(mp, t, r));
+  const uint64_t least = t > 0.f ? sm_min_weight(mp) : 0ull;   // weight that min-p asks for
+  // the tokens that may be kept, in index order: most rows keep few, and their weights are then
+  // computed by full warps
+  const T* val = reinterpret_cast<const T*>(row) + phase;
+  uint16_t* kept = list[warp];
+  int n = 0;
+#pragma unroll 4
+  for (int i0 = 0; i0 < a.V; i0 += 32) {
+    const int i = i0 + lane;
+    const bool in = i < a.V && (float)val[i] >= from;
+    const unsigned m = __ballot_sync(0xffffffffu, in);
+    if (in) kept[n + __popc(m & ((1u << lane) - 1u))] = (uint16_t)i;
+    n += __popc(m);
+  }
+  __syncwarp();
+  auto weight = [&](int j) -> uint64_t {
+    if (j >= n) return 0ull;
     int bin;
-    return x >= from ? (t == 0.f ? 1ull : sm_weight(x, r, table, bin)) : 0ull;
+    const uint64_t w = t == 0.f ? 1ull : sm_weight((float)val[kept[j]], r, table, bin);
+    return w >= least ? w : 0ull;
   };
-  // per 32 vectors (they are contiguous), the warp's sum
-  uint64_t part[NS], total = 0;
+  uint64_t total = 0;
+  for (int j = lane; j < n; j += 32) total += weight(j);
 #pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    part[i] = 0;
-#pragma unroll
-    for (int h = 0; h < G; ++h) {
-      float x[4];
-      Vv::get(q[i], h, x);
-      if (fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= from)
-        part[i] += (weight(x[0]) + weight(x[1])) + (weight(x[2]) + weight(x[3]));
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < NS; ++i) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) part[i] += __shfl_xor_sync(0xffffffffu, part[i], o);
-    total += part[i];
-  }
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   const uint64_t target = t == 0.f ? 0ull : min((uint64_t)(un * (double)total), total - 1);
   uint64_t run = 0;
+  for (int j0 = 0; j0 < n && run <= target; j0 += 32) {
+    const uint64_t w = weight(j0 + lane);
+    uint64_t inc = w;
 #pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    if (run <= target && run + part[i] > target) {
-      uint64_t w[Vv::N], sum = 0;
-#pragma unroll
-      for (int h = 0; h < G; ++h) {
-        float x[4];
-        Vv::get(q[i], h, x);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum += w[4 * h + e] = weight(x[e]);
-      }
-      uint64_t inc = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t b = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += b;
-      }
-      uint64_t at = run + inc - sum;
-      if (at <= target && at + sum > target) {
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-          float x[4];
-          Vv::get(q[i], h, x);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (at <= target && at + w[4 * h + e] > target) {
-              a.ids[rw] = (lane + 32 * i) * Vv::N + 4 * h + e - phase;
-              if (a.prob) a.prob[rw] = sm_prob(x[e], top, t, total);
-            }
-            at += w[4 * h + e];
-          }
-        }
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t b = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += b;
     }
-    run += part[i];
+    if (run + inc > target && run + inc - w <= target) {
+      const int i = kept[j0 + lane];
+      a.ids[rw] = i;
+      if (a.prob) a.prob[rw] = sm_prob((float)val[i], r, table, t, total);
+    }
+    run += __shfl_sync(0xffffffffu, inc, 31);
   }
 }
 
@@ -904,7 +896,7 @@ cudaError_t sm_choose(SmArgs a, int64_t rows, cudaStream_t st) {
   constexpr size_t kHalf = 113 * 1024;      // two CTAs a SM
   const auto bytes = [&](int C) { return ((size_t)((a.V + C - 1) / C) * sizeof(T) + 31) / 16 * 16; };
   if (a.V <= kSmWarpV && !a.top_k && !a.top_p) {
-    sample_warp_kernel<T><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(a, rows);
+    sample_warp_kernel<T><<<(unsigned)((rows + kSmWarps - 1) / kSmWarps), 32 * kSmWarps, 0, st>>>(a, rows);
     return cudaGetLastError();
   }
   if (a.V <= 4096) {
