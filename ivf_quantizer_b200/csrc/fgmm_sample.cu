@@ -79,14 +79,9 @@ __device__ __forceinline__ float sm_max_nan(float a, float b) {
   return r;
 }
 
-// (double)x for a normal number: the conversion instruction runs at a quarter of the rate of fp64
-// arithmetic.  0 and subnormal logits read as less than 2^-126 in magnitude, which moves no weight;
-// infinity reads as 2^128, so that a row whose maximum is infinite needs no case of its own.
-__device__ __forceinline__ double sm_double(float x) {
-  const uint32_t b = __float_as_uint(x);
-  return __hiloint2double((int)((b & 0x80000000u) | (((b & 0x7fffffffu) >> 3) + 0x38000000u)),
-                          (int)(b << 29));
-}
+// (double)x with infinity read as the largest finite value, so that a row whose maximum is infinite
+// needs no case of its own (only its infinite logits are not below `least`).
+__device__ __forceinline__ double sm_double(float x) { return (double)fminf(x, 3.402823466e38f); }
 
 // What a row's weights need.
 struct SmRow {
@@ -638,9 +633,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
         uint64_t w[4];
         int bin[4];
         z.weights(x, w, bin);
+        if (border == kSmAll) {             // (the usual case, kept short: this pass is bound by issue)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (x[e] > from || (x[e] == from && i + e <= il)) z.add(&s.h.lo[bin[e]], &s.h.hi[bin[e]], w[e]);
+          for (int e = 0; e < 4; ++e)
+            if (x[e] >= from) z.add(&s.h.lo[bin[e]], &s.h.hi[bin[e]], w[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (x[e] > from || (x[e] == from && i + e <= il))
+              z.add(&s.h.lo[bin[e]], &s.h.hi[bin[e]], w[e]);
+        }
       });
       z.exchange(true, false);
       uint64_t whole = 0, m = 0;
@@ -904,7 +906,7 @@ cudaError_t sm_choose(SmArgs a, int64_t rows, cudaStream_t st) {
     return sm_launch<T, kSmall, true>(a, rows, 1, kFixedSmall + bytes(1), st);
   }
   int C = 1;
-  while (C < 8 && rows * C < sms && a.V / C > 4096) C *= 2;
+  while (C < 8 && (a.V / C > 32768 || (rows * C < sms && a.V / C > 4096))) C *= 2;
   a.slice = (a.V + C - 1) / C;
   if (rows * C > INT32_MAX) return cudaErrorInvalidValue;
   if (kFixed + bytes(C) <= kHalf)
