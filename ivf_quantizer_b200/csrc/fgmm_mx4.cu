@@ -7,6 +7,8 @@
 //   scores  out = alpha Q X^T + bias over the decoded values
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "fgmm_internal.h"
 #include "sm100_ptx.cuh"
 
@@ -17,48 +19,25 @@ constexpr int kMxThreads = 256;
 
 __device__ __forceinline__ float mx_ld(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float mx_ld(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void mx_ld4(const float* p, float (&v)[4]) {
-  const float4 t = __ldcs(reinterpret_cast<const float4*>(p));
-  v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
-}
-__device__ __forceinline__ void mx_ld4(const __nv_bfloat16* p, float (&v)[4]) {
-  const uint2 t = __ldcs(reinterpret_cast<const uint2*>(p));
-  v[0] = __uint_as_float(t.x << 16), v[1] = __uint_as_float(t.x & 0xffff0000u);
-  v[2] = __uint_as_float(t.y << 16), v[3] = __uint_as_float(t.y & 0xffff0000u);
-}
 __device__ __forceinline__ void mx_st(float* p, float v) { *p = v; }
 __device__ __forceinline__ void mx_st(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void mx_st4(float* p, const float (&v)[4]) {
-  __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
-}
-__device__ __forceinline__ void mx_st4(__nv_bfloat16* p, const float (&v)[4]) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-  uint2 t;
-  t.x = reinterpret_cast<const uint32_t&>(a);
-  t.y = reinterpret_cast<const uint32_t&>(b);
-  __stcs(reinterpret_cast<uint2*>(p), t);
-}
 
 // Four values, already scaled, to four e2m1 codes (nearest, ties to even, saturating).
-__device__ __forceinline__ uint32_t mx_codes4(const float (&v)[4]) {
+__device__ __forceinline__ uint32_t mx_codes4(float a, float b, float c, float d) {
   uint32_t r;
   asm("{\n\t.reg .b8 a, b;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
       "mov.b32 %0, {a, b, a, b};\n\t}"
       : "=r"(r)
-      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]));
+      : "f"(a), "f"(b), "f"(c), "f"(d));
   return r & 0xffffu;
 }
-// Four e2m1 codes (the low 16 bits) to their values.  The three magnitude bits (two of exponent,
-// bias 1, one of mantissa) placed at the top of a float's mantissa and the bottom of its exponent
-// read as the value times 2^-126, the subnormal 0.5 included.
-__device__ __forceinline__ void mx_values4(uint32_t c, float (&v)[4]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t b = c >> (4 * j);
-    v[j] = __uint_as_float((b & 7u) << 22 | (b & 8u) << 28) * 8.507059173023462e37f;  // 2^126
-  }
+// Value of the code in the low four bits.  The three magnitude bits (two of exponent, bias 1, one of
+// mantissa) placed at the top of a float's mantissa and the bottom of its exponent read as the value
+// times 2^-126, the subnormal 0.5 included.
+__device__ __forceinline__ float mx_value(uint32_t b) {
+  return __uint_as_float((b & 7u) << 22 | (b & 8u) << 28) * 8.507059173023462e37f;  // 2^126
 }
 // The value of an e8m0 scale byte.
 __device__ __forceinline__ float mx_scale(uint32_t s) {
@@ -66,111 +45,185 @@ __device__ __forceinline__ float mx_scale(uint32_t s) {
                    : (s == 0u ? __int_as_float(0x00400000) : __int_as_float((int)(s << 23)));
 }
 
-// One warp encodes 128 dimensions (four blocks) of the rows r, r + 32, r + 64, r + 96 of a
-// 128-row tile: four dimensions a lane, eight lanes a block.  Four independent loads a lane are
-// in flight, a row's 128 values are one contiguous read, and the sixteen scales are the 16
-// contiguous bytes that the scale tile gives these rows.  VEC: rows allow 4-value loads.
+// Pieces of 32 bytes of a row: what a thread encodes or decodes at once.
+template <typename T>
+struct MxPiece;
+template <>
+struct MxPiece<float> {
+  static constexpr int N = 8;
+  using Codes = uint32_t;
+  // the piece's largest magnitude as the bits of a float (NaN and infinity sort above the finite)
+  static __device__ __forceinline__ uint32_t top(const uint32_t (&w)[8]) {
+    uint32_t a = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a = max(a, w[j] & 0x7fffffffu);
+    return a;
+  }
+  static __device__ __forceinline__ float at(const uint32_t (&w)[8], int j) { return __uint_as_float(w[j]); }
+  static __device__ __forceinline__ void put(uint32_t (&w)[8], int j, float v) { w[j] = __float_as_uint(v); }
+};
+template <>
+struct MxPiece<__nv_bfloat16> {
+  static constexpr int N = 16;
+  using Codes = uint64_t;
+  static __device__ __forceinline__ uint32_t top(const uint32_t (&w)[8]) {
+    uint32_t a = 0;                         // both halves of a word at once
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a = __vmaxu2(a, w[j] & 0x7fff7fffu);
+    return max(a << 16, a & 0xffff0000u);
+  }
+  static __device__ __forceinline__ float at(const uint32_t (&w)[8], int j) {
+    return __uint_as_float(j & 1 ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
+  }
+  static __device__ __forceinline__ void put(uint32_t (&w)[8], int j, float v) {
+    const uint32_t b = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    if (j & 1) w[j >> 1] |= b << 16;
+    else w[j >> 1] = b;
+  }
+};
+
+// The pieces of a thread: piece i of the padded rows (nb blocks each) with stride `step`.
+struct MxPieces {
+  int64_t i, row, drow, step;
+  int seg, dseg, segs;
+  __device__ __forceinline__ MxPieces(int segs_) : segs(segs_) {
+    i = (int64_t)blockIdx.x * kMxThreads + threadIdx.x;
+    step = (int64_t)gridDim.x * kMxThreads;
+    row = i / segs, seg = (int)(i - row * segs);
+    drow = step / segs, dseg = (int)(step - drow * segs);
+  }
+  __device__ __forceinline__ void next() {
+    i += step, row += drow, seg += dseg;
+    if (seg >= segs) seg -= segs, ++row;
+  }
+};
+__device__ __forceinline__ int64_t mx_scale_at(int64_t row, int b, int nkc) {
+  return ((row >> 7) * nkc + (b >> 2)) * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4 + (b & 3);
+}
+
+// A thread encodes 32 bytes of a row at a time, four (fp32) or two (bf16) neighbouring lanes a block;
+// codes lie in the order of the threads, so a warp writes them as one contiguous piece.  Two pieces a
+// thread are loaded before either is used.  Bound by memory; a lane a 4 values took
+// 1266 us at 10^6 x 960 bf16 (issue), this takes MEASURE.  VEC: rows allow 16-byte loads.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kMxThreads)
     mx4_encode_kernel(const T* __restrict__ X, int64_t n, int D, int64_t ldx, int nb, int nkc,
-                      int64_t groups, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
-  const int lane = threadIdx.x & 31;
-  const int64_t step = (int64_t)gridDim.x * (kMxThreads / 32);
-  for (int64_t g = (int64_t)blockIdx.x * (kMxThreads / 32) + (threadIdx.x >> 5); g < groups;
-       g += step) {
-    const int64_t rr = g / nkc;                 // row tile * 32 + row within the quarter
-    const int kc = (int)(g - rr * nkc);
-    const int64_t row0 = (rr >> 5) * 128 + (rr & 31);
-    const int d = kc * 128 + lane * 4;
-    float v[4][4];
+                      uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  using P = MxPiece<T>;
+  constexpr int LB = 32 / P::N, U = 2;      // lanes a block, pieces in flight
+  MxPieces p(nb * LB);
+  const int64_t rows = (n + 127) / 128 * 128;   // rows behind the last only have scales, 0
+  // (whole warps stay together for the exchange: a warp leaves when its first piece is behind the end)
+  const int64_t pieces = rows * nb * LB;
+  while (p.i - (threadIdx.x & 31) < pieces) {
+    uint32_t w[U][8];
+    int64_t at[U], row[U];
+    int seg[U];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int64_t row = row0 + 32 * c;
-      const T* p = X + row * ldx + d;
+    for (int u = 0; u < U; ++u) {
+      at[u] = p.i, row[u] = p.row, seg[u] = p.seg;
+      p.next();
+      const int d = seg[u] * P::N;
+      const T* x = X + row[u] * ldx + d;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[c][j] = 0.f;
-      if (row < n) {
-        if (VEC && d + 4 <= D) {
-          mx_ld4(p, v[c]);
+      for (int j = 0; j < 8; ++j) w[u][j] = 0u;
+      if (row[u] < n) {
+        if (VEC && d + P::N <= D) {
+          const uint4 a = __ldcs(reinterpret_cast<const uint4*>(x));
+          const uint4 b = __ldcs(reinterpret_cast<const uint4*>(x) + 1);
+          w[u][0] = a.x, w[u][1] = a.y, w[u][2] = a.z, w[u][3] = a.w;
+          w[u][4] = b.x, w[u][5] = b.y, w[u][6] = b.z, w[u][7] = b.w;
         } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (d + j < D) v[c][j] = mx_ld(p + j);
+          for (int j = 0; j < P::N; ++j)
+            if (d + j < D) P::put(w[u], j, mx_ld(x + j));
+            else if (j % 2 == 0 || P::N == 8) P::put(w[u], j, 0.f);
         }
       }
     }
-    uint32_t words[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      // magnitudes as integers: NaN and infinity sort above every finite value
-      uint32_t a = 0;
+    for (int u = 0; u < U; ++u) {
+      uint32_t a = P::top(w[u]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) a = max(a, __float_as_uint(v[c][j]) & 0x7fffffffu);
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+      for (int o = 1; o < LB; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
       const uint32_t e = a >> 23;
-      uint32_t s = e > 2u ? e - 2u : 0u;        // floor(log2 a) - 2 + 127, at least 0
-      const float inv = __uint_as_float((254u - s) << 23);
-      float y[4];
+      const bool bad = e == 255u;
+      const uint32_t s = bad ? 255u : e > 2u ? e - 2u : 0u;   // floor(log2 a) - 2 + 127, at least 0
+      const float inv = __uint_as_float((bad ? 0u : 254u - s) << 23);
+      typename P::Codes c = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = v[c][j] * inv;
-      uint32_t code = mx_codes4(y);
-      if (e == 255u) s = 255u, code = 0u;
-      const int64_t row = row0 + 32 * c;
-      if (row < n && d < nb * 32)
-        *reinterpret_cast<uint16_t*>(codes + row * ((int64_t)nb * 16) + (d >> 1)) = (uint16_t)code;
-      uint32_t w = s << (8 * (lane >> 3));
-      w |= __shfl_xor_sync(0xffffffffu, w, 8);
-      w |= __shfl_xor_sync(0xffffffffu, w, 16);
-      words[c] = w;
+      for (int j = 0; j < P::N; j += 4)
+        c |= (typename P::Codes)mx_codes4(P::at(w[u], j) * inv, P::at(w[u], j + 1) * inv,
+                                          P::at(w[u], j + 2) * inv, P::at(w[u], j + 3) * inv)
+             << (4 * j);
+      if (bad) c = 0;
+      if (at[u] >= pieces) continue;
+      if (row[u] < n) reinterpret_cast<typename P::Codes*>(codes)[at[u]] = c;
+      const int b = seg[u] / LB;
+      if (seg[u] % LB == 0) {
+        scales[mx_scale_at(row[u], b, nkc)] = row[u] < n ? (uint8_t)s : 0;
+        if (b == nb - 1)                    // and the padding of the last scale tile
+          for (int z = nb; z < 4 * nkc; ++z) scales[mx_scale_at(row[u], z, nkc)] = 0;
+      }
     }
-    if (lane == 0)
-      *reinterpret_cast<uint4*>(scales + ((rr >> 5) * nkc + kc) * 512 + (rr & 31) * 16) =
-          make_uint4(words[0], words[1], words[2], words[3]);
   }
 }
 
-// The same assignment of rows and dimensions to warps and lanes as in mx4_encode_kernel.
+// One warp decodes 512 bytes of output (128 fp32 or 256 bf16 dimensions) of the rows r, r + 32,
+// r + 64, r + 96 of a 128-row tile: 16 bytes a lane and row, and the four rows' scales of a block lie
+// in the same 16 bytes of the scale tile.  Bound by writing; with the encoder's mapping (a flat
+// sequence of pieces) the address arithmetic of every 16 bytes took it to 979 us at 10^6 x 960 fp32,
+// against MEASURE.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kMxThreads)
     mx4_decode_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                      int64_t n, int D, int nb, int nkc, int64_t groups, T* __restrict__ out,
+                      int64_t n, int D, int nb, int nkc, int nkg, int64_t groups, T* __restrict__ out,
                       int64_t ldo) {
+  constexpr int N = 16 / sizeof(T);
+  using Codes = std::conditional_t<N == 4, uint16_t, uint32_t>;
   const int lane = threadIdx.x & 31;
   const int64_t step = (int64_t)gridDim.x * (kMxThreads / 32);
-  for (int64_t g = (int64_t)blockIdx.x * (kMxThreads / 32) + (threadIdx.x >> 5); g < groups;
-       g += step) {
-    const int64_t rr = g / nkc;
-    const int kc = (int)(g - rr * nkc);
+  for (int64_t g = (int64_t)blockIdx.x * (kMxThreads / 32) + (threadIdx.x >> 5); g < groups; g += step) {
+    const int64_t rr = g / nkg;                     // row tile * 32 + row within the quarter
+    const int kg = (int)(g - rr * nkg), d = (kg * 32 + lane) * N;
+    if (d >= D) continue;
     const int64_t row0 = (rr >> 5) * 128 + (rr & 31);
-    const int d = kc * 128 + lane * 4;
     const uint4 sw = __ldg(reinterpret_cast<const uint4*>(
-        scales + ((rr >> 5) * nkc + kc) * 512 + (rr & 31) * 16));
+        scales + ((rr >> 5) * nkc + (d >> 7)) * 512 + (rr & 31) * 16));
     const uint32_t words[4] = {sw.x, sw.y, sw.z, sw.w};
-    uint32_t code[4];
+    const uint8_t* from = codes + row0 * nb * 16 + (d >> 1);
+    uint32_t c[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int64_t row = row0 + 32 * c;
-      code[c] = (row < n && d < D) ? __ldcs(reinterpret_cast<const uint16_t*>(
-                                         codes + row * ((int64_t)nb * 16) + (d >> 1)))
-                                   : 0u;
-    }
+    for (int q = 0; q < 4; ++q)
+      c[q] = row0 + 32 * q < n
+                 ? (uint32_t)__ldcs(reinterpret_cast<const Codes*>(from + (int64_t)32 * q * nb * 16)) : 0u;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int64_t row = row0 + 32 * c;
-      if (row >= n) continue;
-      const float s = mx_scale((words[c] >> (8 * (lane >> 3))) & 255u);
-      float v[4];
-      mx_values4(code[c], v);
+    for (int q = 0; q < 4; ++q) {
+      if (row0 + 32 * q >= n) break;
+      const float s = mx_scale((words[q] >> (d >> 2 & 24)) & 255u);
+      T* o = out + (row0 + 32 * q) * ldo + d;
+      float v[N];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] *= s;
-      T* p = out + row * ldo + d;
-      if (VEC && d + 4 <= D) {
-        mx_st4(p, v);
+      for (int j = 0; j < N; ++j) v[j] = mx_value(c[q] >> (4 * j)) * s;
+      if (VEC && d + N <= D) {
+        uint4 w;
+        if constexpr (N == 4) {
+          w = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                         __float_as_uint(v[3]));
+        } else {
+          uint32_t h[4];                            // (exact: a code has two significant bits)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+            h[j] = reinterpret_cast<const uint32_t&>(t);
+          }
+          w = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        __stcs(reinterpret_cast<uint4*>(o), w);
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (d + j < D) mx_st(p + j, v[j]);
+        for (int j = 0; j < N; ++j)
+          if (d + j < D) mx_st(o + j, v[j]);
       }
     }
   }
@@ -179,53 +232,217 @@ __global__ void __launch_bounds__(kMxThreads)
 // ------------------------------------------------------------------ scores (tcgen05)
 // The vectors are the M side of the products (128 of them a tile: TMEM lane = vector), the
 // queries the N side (NT a tile: TMEM column = query).  The codes then stream through the wide
-// side whatever the number of queries, and a warp's 32 lanes write 32 consecutive scores of one
-// query: whole 128-byte lines from registers, for any N and any row stride.
+// side whatever the number of queries, and a warp holds 32 consecutive scores of one query.
 //
-// One CTA a SM walks its tiles: a TMA warp fills a ring of stages (256 dimensions of 128 vectors
-// and NT queries, 128 bytes a row, and their scale tiles), one thread copies a stage's scales to
-// TMEM and issues its four K = 64 block-scaled products, and the epilogue warps drain one of two
-// accumulators while the other is filled.
+// A CTA walks its tiles: a producer thread fills a ring of stages (KB bytes of each of 128 vectors
+// and their scale tiles), one thread copies a stage's scales to TMEM and issues its K = 64
+// block-scaled products, and the epilogue warps drain one of two accumulators while the other is
+// filled.  Two kernels differ in how a stage is filled:
+//   rows longer than 256 dimensions: TMA boxes of 128 vectors x 128 bytes, with the queries' beside;
+//   shorter ones: a tile is one contiguous piece of memory, so it comes as a single bulk copy, and
+//   two warps put it into the swizzled order.  TMA takes about 4 cycles a row of a box whatever
+//   its length (9 where rows are not a multiple of 64 bytes), which bound these tiles: 17.6 and 33 us
+//   for one query against 10^6 vectors of 128 and of 96 dimensions.  The queries' tile stays in
+//   shared memory while the vectors' tiles go by.
+//
+// The output is the larger part of the traffic for short rows.  Scores written straight from
+// registers are 128-byte pieces that straddle two lines when the row stride is odd (156 us against
+// 84 aligned, 1000 x 100003 x 128 fp32), so tiles of 64 queries and more pass through shared memory
+// and leave as bulk copies of a query's 128 scores, the ragged ends aside.
 constexpr int kMxBM = 128;         // vectors a tile
-constexpr int kMxRowB = 128;       // bytes of a row in a stage: 256 dimensions
-constexpr int kMxSfB = 1024;       // scale bytes of 128 rows in a stage: two tiles of 512
+constexpr int kMxMaxStages = 10;
 
+// What both kernels share: the epilogue's side.
 template <int NT>
-struct MxCfg {
-  static constexpr int kStage = kMxBM * kMxRowB + NT * kMxRowB + 2 * kMxSfB;
-  static constexpr int kStages = (216 * 1024) / kStage < 10 ? (216 * 1024) / kStage : 10;
-  static constexpr int kEpiWarps = NT >= 64 ? 8 : 4;
-  static constexpr int kThreads = 128 + 32 * kEpiWarps;
+struct MxEpi {
+  static constexpr bool kStaged = NT >= 64;
+  static constexpr int kWarps = kStaged ? NT / 8 : 4;         // four of them for 32 queries
+  static constexpr int kThreads = 128 + 32 * kWarps;
+  // staging: two buffers of 16 queries x (128 scores + 16 bytes) for each four warps
+  static constexpr int kOutRow = 128 * 4 + 16;
+  static constexpr int kOut = kStaged ? kWarps / 4 * 2 * 16 * kOutRow : 0;
+};
+
+template <int NT, int KB>
+struct MxCfg : MxEpi<NT> {
+  static constexpr int kAtoms = KB / 64, kSfB = 512 * kAtoms;   // scale tiles a stage and side
+  static constexpr int kStage = kMxBM * KB + NT * KB + 2 * kSfB;
+  static constexpr int kCtas = NT >= 128 ? 1 : KB == 64 ? (NT == 64 ? 2 : 4) : (NT == 64 ? 1 : 2);
+  static constexpr int kBudget = (kCtas == 1 ? 226 : kCtas == 2 ? 112 : 55) * 1024 - 1024 - 512 -
+                                 MxEpi<NT>::kOut;
+  static constexpr int kStages = kBudget / kStage < kMxMaxStages ? kBudget / kStage : kMxMaxStages;
+  static constexpr int kSmem = 1024 + kStages * kStage + MxEpi<NT>::kOut + 512;
   static constexpr int kCols = NT == 128 ? 512 : 4 * NT < 64 ? 64 : 4 * NT;  // TMEM columns
-  static constexpr int kSfCol = 2 * NT;             // two scale sets of 16 columns behind the sums
+  static constexpr int kSfCol = 2 * NT;             // 32 columns of scales behind the sums
+  static_assert(kStages >= 3 && kSfCol + 32 <= kCols && kCols * kCtas <= 512, "tile");
+};
+
+template <int NT, int KB>
+struct MxPackCfg : MxEpi<NT> {
+  static constexpr int kAtoms = KB / 64, kSfB = 512 * kAtoms;
+  // vector tiles a step: with few queries a step's work is short against its barriers
+  static constexpr int kSub = NT <= 32 && KB == 64 ? 2 : 1;
+  static constexpr int kOne = kMxBM * KB + kSfB;    // a tile as it comes, and as the products read it
+  static constexpr int kTile = kSub * kOne;
+  static constexpr int kQ = NT * KB + kSfB;         // the queries' tile
+  static constexpr int kMoveWarps = NT <= 32 ? 4 : 2;
+  static constexpr int kThreads = MxEpi<NT>::kThreads + 32 * (kMoveWarps - 2);
+  static constexpr int kCtas = NT == 128 || (NT == 64 && KB == 128) ? 1 : 2;
+  static constexpr int kBufs = 2;                   // swizzled stages and accumulators
+  static constexpr int kBudget = (kCtas == 1 ? 226 : 112) * 1024 - 1024 - 512 - MxEpi<NT>::kOut -
+                                 kBufs * kTile - 2 * kQ;
+  static constexpr int kRaw = kBudget / kTile < kMxMaxStages ? kBudget / kTile : kMxMaxStages;
+  static constexpr int kSmem = 1024 + (kRaw + kBufs) * kTile + 2 * kQ + MxEpi<NT>::kOut + 512;
+  // TMEM: the accumulators, the vectors' scales, the queries'
+  static constexpr int kSfA = kBufs * kSub * NT, kSfQ = kSfA + kBufs * kSub * 4 * kAtoms;
+  static constexpr int kNeed = kSfQ + 2 * 4 * kAtoms;
+  static constexpr int kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
+  static_assert(kRaw >= 2 && kNeed <= 512 && kCols * kCtas <= 512, "tile");
 };
 
 struct MxBars {
-  uint64_t full[10], empty[10], s_full[2], s_empty[2], drain;
+  uint64_t full[kMxMaxStages], empty[kMxMaxStages];   // the ring
+  uint64_t swz_full[3], swz_empty[3], q_full[2], q_empty[2];
+  uint64_t s_full[3], s_empty[3], drain;              // accumulators
   uint32_t tmem;
   int abort;
 };
+static_assert(sizeof(MxBars) <= 512, "barriers");
 
 __device__ __forceinline__ void mx_timeout(int* status, MxBars* bars) {
   if (status) atomicCAS(status, FGMM_OK, FGMM_ERR_TIMEOUT);
   bars->abort = 1;
 }
 
-template <int NT, typename T>
-__global__ void __launch_bounds__(MxCfg<NT>::kThreads, 1)
+// The tiles of a CTA.  QFAST: queries fastest, so that a tile of long vectors is read from memory
+// once; else vectors fastest, so that the queries' tile stays.
+template <bool QFAST>
+struct MxWalk {
+  int64_t fast, slow, nfast, nslow, dfast, dslow;
+  __device__ __forceinline__ MxWalk(int64_t vtiles, int64_t qtiles)
+      : nfast(QFAST ? qtiles : vtiles), nslow(QFAST ? vtiles : qtiles) {
+    fast = blockIdx.x % nfast, slow = blockIdx.x / nfast;
+    dfast = gridDim.x % nfast, dslow = gridDim.x / nfast;
+  }
+  __device__ __forceinline__ bool more() const { return slow < nslow; }
+  __device__ __forceinline__ void next() {
+    fast += dfast, slow += dslow;
+    if (fast >= nfast) fast -= nfast, ++slow;
+  }
+  __device__ __forceinline__ int64_t v() const { return QFAST ? slow : fast; }
+  __device__ __forceinline__ int64_t q() const { return QFAST ? fast : slow; }
+};
+
+__device__ __forceinline__ void mx_cvt(float v, float& o) { o = v; }
+__device__ __forceinline__ void mx_cvt(float v, __nv_bfloat16& o) { o = __float2bfloat16_rn(v); }
+
+// The epilogue warps (`warp` from 0, a multiple of 4 in the CTA) of a CTA: scale, bias, rounding and
+// the stores of every step of SUB vector tiles.
+template <int NT, int SUB, int BUFS, bool QFAST, typename T>
+__device__ __forceinline__ void mx_epilogue(int warp, MxBars* bars, unsigned char* outbuf, uint32_t tmem, int64_t n,
+                                            int64_t m, int64_t vtiles, int64_t qtiles, float alpha,
+                                            const float* __restrict__ bias, T* __restrict__ out,
+                                            int64_t ldo, int* status) {
+  using C = MxEpi<NT>;
+  volatile int* abort = &bars->abort;
+  const int lane = threadIdx.x & 31;
+  constexpr int kColsWarp = NT * 4 / C::kWarps;          // columns a warp drains
+  constexpr int kChunk = C::kStaged || kColsWarp < 32 ? 16 : 32;
+  const int q = warp & 3, grp = warp >> 2, c0 = grp * kColsWarp;
+  const uint32_t lane_base = (uint32_t)(q * 32) << 16;
+  uint32_t buf = BUFS - 1, use = 1;                      // buffer and parity of its phase
+  for (MxWalk<QFAST> w(vtiles, qtiles); w.more(); w.next()) {
+    const int64_t m0 = w.q() * NT + c0;
+    if (++buf == BUFS) buf = 0, use ^= 1;
+    float bvs[SUB];
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) {
+      const int64_t row = (w.v() * SUB + u) * kMxBM + q * 32 + lane;
+      bvs[u] = bias && row < n ? __ldg(bias + row) : 0.f;
+    }
+    bool ok = ptx::mbar_wait_warp(&bars->s_full[buf], use, abort);
+    if (!ok) mx_timeout(status, bars);
+    // the four warps of a group meet at barriers below: they go on or give up together
+    if constexpr (C::kStaged) ok = ptx::named_all(1 + grp, 128, ok);
+    if (!ok) break;
+    ptx::tc_fence_after();
+#pragma unroll
+    for (int sub = 0; sub < SUB; ++sub) {
+    const int64_t n0 = (w.v() * SUB + sub) * kMxBM, row = n0 + q * 32 + lane;
+    const float bv = bvs[sub];
+    const uint32_t acc = tmem + lane_base + (buf * SUB + sub) * NT + c0;
+#pragma unroll
+    for (int c = 0; c < kColsWarp; c += kChunk) {
+      uint32_t u[kChunk];
+      if constexpr (kChunk == 32) ptx::tmem_ld32(acc + c, u);
+      else ptx::tmem_ld16(acc + c, u);
+      ptx::tmem_wait_ld();
+      if (sub + 1 == SUB && c + kChunk == kColsWarp) {  // all in registers: hand the accumulator back
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars->s_empty[buf]);
+      }
+      const int64_t mc = m0 + c;
+      const int rows = (int)min((int64_t)kChunk, m - mc);   // queries of the chunk (may be <= 0)
+      if constexpr (C::kStaged) {
+        constexpr int VN = 16 / sizeof(T);
+        unsigned char* st = outbuf + (grp * 2 + ((c / kChunk) & 1)) * kChunk * C::kOutRow;
+        // element (query r, vector i) of the chunk lies at st[r][phase_r + i], phase_r being what
+        // its row's address is off a 16-byte boundary
+        const int p0 = (int)(((uintptr_t)out / sizeof(T) + (uintptr_t)mc * ldo + n0) % VN);
+        const int dp = (int)(ldo % VN);
+        ptx::bulk_wait_read<1>();           // the buffer's last copies have read it
+        ptx::named_sync(1 + grp, 128);
+        T* mine = reinterpret_cast<T*>(st) + q * 32 + lane;
+#pragma unroll
+        for (int e = 0; e < kChunk; ++e)
+          mx_cvt(fmaf(alpha, __uint_as_float(u[e]), bv),
+                 mine[e * (C::kOutRow / sizeof(T)) + ((p0 + e * dp) & (VN - 1))]);
+        ptx::fence_proxy_async_smem();
+        ptx::named_sync(1 + grp, 128);
+        // four queries a warp, eight lanes each: one copies the aligned inside of the row, all
+        // write what lies before and behind it
+        const int r = 4 * q + (lane >> 3), ph = (p0 + r * dp) & (VN - 1);
+        const int end = ph + (int)min((int64_t)kMxBM, n - n0);
+        const int a0 = (ph + VN - 1) & ~(VN - 1), a1 = end & ~(VN - 1);
+        if (r < rows) {
+          const T* from = reinterpret_cast<const T*>(st + r * C::kOutRow);
+          T* to = out + (mc + r) * ldo + n0 - ph;
+          if ((lane & 7) == 0 && a1 > a0)
+            ptx::bulk_store(to + a0, ptx::smem_u32(from + a0), (uint32_t)(a1 - a0) * sizeof(T));
+          const int i = lane & 7;
+          if (i >= ph && i < min(a0, end)) to[i] = from[i];
+          if (max(a0, a1) + i < end) to[max(a0, a1) + i] = from[max(a0, a1) + i];
+        }
+        ptx::bulk_commit();
+      } else if (row < n) {
+        T* o = out + mc * ldo + row;
+#pragma unroll
+        for (int e = 0; e < kChunk; ++e, o += ldo)
+          if (e < rows) mx_st(o, fmaf(alpha, __uint_as_float(u[e]), bv));
+      }
+    }
+    }
+  }
+  if constexpr (C::kStaged) ptx::bulk_wait_read<0>();
+}
+
+template <int NT, int KB, typename T>
+__global__ void __launch_bounds__(MxEpi<NT>::kThreads, MxCfg<NT, KB>::kCtas)
     mx4_scores_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmq,
                       const uint8_t* __restrict__ xs, const uint8_t* __restrict__ qs, int64_t n,
-                      int64_t m, int nb, int64_t ntiles, int mtiles, float alpha,
+                      int64_t m, int nb, int64_t vtiles, int64_t qtiles, float alpha,
                       const float* __restrict__ bias, T* __restrict__ out, int64_t ldo, int* status) {
-  using C = MxCfg<NT>;
+  using C = MxCfg<NT, KB>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* ring = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  MxBars* bars = reinterpret_cast<MxBars*>(ring + C::kStages * C::kStage);
+  unsigned char* outbuf = ring + C::kStages * C::kStage;
+  MxBars* bars = reinterpret_cast<MxBars*>(outbuf + C::kOut);
   volatile int* abort = &bars->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nkc = (nb + 3) / 4;                     // scale tiles (128 dimensions) of a row
-  const int nst = (nkc + 1) / 2;                    // stages of a tile
+  const int nst = (nkc + C::kAtoms - 1) / C::kAtoms;  // stages of a tile
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       ptx::mbar_init(&bars->full[s], 1);
@@ -233,7 +450,7 @@ __global__ void __launch_bounds__(MxCfg<NT>::kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(&bars->s_full[b], 1);
-      ptx::mbar_init(&bars->s_empty[b], C::kEpiWarps);
+      ptx::mbar_init(&bars->s_empty[b], C::kWarps);
     }
     ptx::mbar_init(&bars->drain, 1);
     bars->abort = 0;
@@ -252,27 +469,28 @@ __global__ void __launch_bounds__(MxCfg<NT>::kThreads, 1)
     if (lane == 0) {
       ptx::prefetch_tmap(&tmx);
       ptx::prefetch_tmap(&tmq);
-      uint32_t it = 0;
+      uint32_t it = 0, s = 0, ph = 1;               // ph: parity of the release to wait for
       bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < ntiles && !*abort; t += gridDim.x) {
-        const int64_t nt = t / mtiles;
-        const int mt = (int)(t - nt * mtiles);
-        for (int k = 0; k < nst; ++k, ++it) {
-          const int s = it % C::kStages;
-          if (it >= C::kStages && !ptx::mbar_wait(&bars->empty[s], ((it / C::kStages) - 1) & 1, abort)) {
+      for (MxWalk<true> w(vtiles, qtiles); ok && w.more() && !*abort; w.next()) {
+        const uint8_t* xsf = xs + w.v() * nkc * 512;
+        const uint8_t* qsf = qs + w.q() * nkc * 512;
+        for (int k = 0; k < nst; ++k) {
+          if (it >= C::kStages && !ptx::mbar_wait(&bars->empty[s], ph, abort)) {
             mx_timeout(status, bars);
             ok = false;
             break;
           }
           unsigned char* a = ring + s * C::kStage;
-          unsigned char* b = a + kMxBM * kMxRowB;
-          unsigned char* sf = b + NT * kMxRowB;
-          const uint32_t sfb = (nkc - 2 * k >= 2 ? 2 : 1) * 512;
-          ptx::mbar_arrive_expect_tx(&bars->full[s], kMxBM * kMxRowB + NT * kMxRowB + 2 * sfb);
-          ptx::tma_load_2d(a, &tmx, &bars->full[s], k * kMxRowB, (int)(nt * kMxBM));
-          ptx::bulk_load(sf, xs + (nt * nkc + 2 * k) * 512, sfb, &bars->full[s]);
-          ptx::tma_load_2d(b, &tmq, &bars->full[s], k * kMxRowB, mt * NT);
-          ptx::bulk_load(sf + kMxSfB, qs + ((int64_t)mt * nkc + 2 * k) * 512, sfb, &bars->full[s]);
+          unsigned char* b = a + kMxBM * KB;
+          unsigned char* sf = b + NT * KB;
+          const uint32_t sfb = min(nkc - C::kAtoms * k, C::kAtoms) * 512;
+          ptx::mbar_arrive_expect_tx(&bars->full[s], kMxBM * KB + NT * KB + 2 * sfb);
+          ptx::tma_load_2d(a, &tmx, &bars->full[s], k * KB, (int)(w.v() * kMxBM));
+          ptx::bulk_load(sf, xsf + k * C::kSfB, sfb, &bars->full[s]);
+          ptx::tma_load_2d(b, &tmq, &bars->full[s], k * KB, (int)(w.q() * NT));
+          ptx::bulk_load(sf + C::kSfB, qsf + k * C::kSfB, sfb, &bars->full[s]);
+          ++it;
+          if (++s == C::kStages) s = 0, ph ^= 1;
         }
       }
       if (*abort)  // let every copy this thread started land before the CTA exits
@@ -281,10 +499,10 @@ __global__ void __launch_bounds__(MxCfg<NT>::kThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      constexpr uint64_t kHiK = ptx::sw128_hi(16, 1024);
-      uint32_t it = 0, j = 0;
+      constexpr uint64_t kHiK = KB == 128 ? ptx::sw128_hi(16, 1024) : ptx::sw64_hi(16, 512);
+      uint32_t s = 0, ph = 0, it = 0, j = 0;
       bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < ntiles && !*abort; t += gridDim.x, ++j) {
+      for (MxWalk<true> w(vtiles, qtiles); ok && w.more() && !*abort; w.next(), ++j) {
         const uint32_t buf = j & 1;
         if (j >= 2 && !ptx::mbar_wait(&bars->s_empty[buf], ((j >> 1) - 1) & 1, abort)) {
           ok = false;
@@ -292,26 +510,28 @@ __global__ void __launch_bounds__(MxCfg<NT>::kThreads, 1)
         }
         const uint32_t d_tmem = tmem + buf * NT;
         for (int k = 0; k < nst; ++k, ++it) {
-          const int s = it % C::kStages;
-          if (!ptx::mbar_wait(&bars->full[s], (it / C::kStages) & 1, abort)) {
+          if (!ptx::mbar_wait(&bars->full[s], ph, abort)) {
             ok = false;
             break;
           }
           const uint32_t a = ptx::smem_u32(ring + s * C::kStage);
-          const uint32_t b = a + kMxBM * kMxRowB, sf = b + NT * kMxRowB;
+          const uint32_t b = a + kMxBM * KB, sf = b + NT * KB;
           const uint32_t sft = tmem + C::kSfCol + (it & 1) * 16;
-          const int steps = min(4, (nb + 1) / 2 - 4 * k);
-          for (int h = 0; h < (steps + 1) / 2; ++h) {
-            ptx::tmem_cp_32x128(sft + 4 * h, ptx::rows16_desc(sf + 512 * h));
-            ptx::tmem_cp_32x128(sft + 8 + 4 * h, ptx::rows16_desc(sf + kMxSfB + 512 * h));
-          }
+          const int steps = min(2 * C::kAtoms, (nb + 1) / 2 - 2 * C::kAtoms * k);
+#pragma unroll
+          for (int h = 0; h < C::kAtoms; ++h)
+            if (2 * h < steps) {
+              ptx::tmem_cp_32x128(sft + 4 * h, ptx::rows16_desc(sf + 512 * h));
+              ptx::tmem_cp_32x128(sft + 8 + 4 * h, ptx::rows16_desc(sf + C::kSfB + 512 * h));
+            }
           const uint64_t da = ptx::sw128_desc(a, kHiK), db = ptx::sw128_desc(b, kHiK);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+          for (int q = 0; q < 2 * C::kAtoms; ++q)
             if (q < steps)
               ptx::mma_mxf4_ss(d_tmem, da + 2 * q, db + 2 * q, ptx::idesc_mxf4(kMxBM, NT, 2 * (q & 1)),
                                sft + 4 * (q >> 1), sft + 8 + 4 * (q >> 1), k > 0 || q > 0);
           ptx::mma_commit(&bars->empty[s]);
+          if (++s == C::kStages) s = 0, ph ^= 1;
         }
         if (ok) ptx::mma_commit(&bars->s_full[buf]);
       }
@@ -322,47 +542,197 @@ __global__ void __launch_bounds__(MxCfg<NT>::kThreads, 1)
       }
     }
   } else if (warp >= 4) {
-    constexpr int kColsWarp = NT * 4 / C::kEpiWarps;          // columns a warp drains
-    constexpr int kChunk32 = kColsWarp < 32 ? 16 : 32;
-    const int q = warp & 3, c0 = ((warp - 4) >> 2) * kColsWarp;
-    const uint32_t lane_base = (uint32_t)(q * 32) << 16;
-    uint32_t j = 0;
-    for (int64_t t = blockIdx.x; t < ntiles && !*abort; t += gridDim.x, ++j) {
-      const int64_t nt = t / mtiles;
-      const int64_t m0 = (t - nt * mtiles) * NT;
-      const uint32_t buf = j & 1;
-      const int64_t row = nt * kMxBM + q * 32 + lane;
-      const float bv = bias && row < n ? __ldg(bias + row) : 0.f;
-      if (!ptx::mbar_wait_warp(&bars->s_full[buf], (j >> 1) & 1, abort)) {
+    mx_epilogue<NT, 1, 2, true, T>(warp - 4, bars, outbuf, tmem, n, m, vtiles, qtiles, alpha, bias, out, ldo, status);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, C::kCols);
+  }
+}
+
+// Rows of at most KB bytes (nb <= KB / 16); vtiles counts steps of kSub vector tiles.
+template <int NT, int KB, typename T>
+__global__ void __launch_bounds__(MxPackCfg<NT, KB>::kThreads, MxPackCfg<NT, KB>::kCtas)
+    mx4_scores_packed_kernel(const __grid_constant__ CUtensorMap tmq, const uint8_t* __restrict__ xc,
+                             const uint8_t* __restrict__ xs, const uint8_t* __restrict__ qs, int64_t n,
+                             int64_t m, int nb, int64_t vtiles, int64_t qtiles, float alpha,
+                             const float* __restrict__ bias, T* __restrict__ out, int64_t ldo,
+                             int* status) {
+  using C = MxPackCfg<NT, KB>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* swz = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  unsigned char* qbuf = swz + C::kBufs * C::kTile;
+  unsigned char* raw = qbuf + 2 * C::kQ;
+  unsigned char* outbuf = raw + C::kRaw * C::kTile;
+  MxBars* bars = reinterpret_cast<MxBars*>(outbuf + C::kOut);
+  volatile int* abort = &bars->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nkc = (nb + 3) / 4;                     // scale tiles (128 dimensions) of a row
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kRaw; ++s) {
+      ptx::mbar_init(&bars->full[s], 1);
+      ptx::mbar_init(&bars->empty[s], C::kMoveWarps);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(&bars->q_full[b], 1);
+      ptx::mbar_init(&bars->q_empty[b], 1);
+    }
+    for (int b = 0; b < C::kBufs; ++b) {
+      ptx::mbar_init(&bars->swz_full[b], C::kMoveWarps);
+      ptx::mbar_init(&bars->swz_empty[b], 1);
+      ptx::mbar_init(&bars->s_full[b], 1);
+      ptx::mbar_init(&bars->s_empty[b], C::kWarps);
+    }
+    ptx::mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    ptx::fence_mbar_init();
+  }
+  // the part of a swizzled row behind its codes stays 0 (and so do rows behind the last vector,
+  // until codes of an earlier tile lie there, whose scores are not written)
+  for (int i = threadIdx.x; i < C::kBufs * C::kTile / 16; i += C::kThreads)
+    reinterpret_cast<uint4*>(swz)[i] = make_uint4(0u, 0u, 0u, 0u);
+  ptx::fence_proxy_async_smem();
+  if (warp == 1) {
+    ptx::tmem_alloc(&bars->tmem, C::kCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      ptx::prefetch_tmap(&tmq);
+      uint32_t it = 0, s = 0, ph = 1, jq = 0;       // ph: parity of the release to wait for
+      int64_t qt = -1;
+      bool ok = true;
+      for (MxWalk<false> w(vtiles, qtiles); ok && w.more() && !*abort; w.next()) {
+        if (w.q() != qt) {                          // the next tile of queries
+          qt = w.q();
+          const uint32_t b = jq & 1;
+          if (jq >= 2 && !ptx::mbar_wait(&bars->q_empty[b], ((jq >> 1) - 1) & 1, abort)) ok = false;
+          if (!ok) break;
+          ptx::mbar_arrive_expect_tx(&bars->q_full[b], NT * KB + nkc * 512);
+          ptx::tma_load_2d(qbuf + b * C::kQ, &tmq, &bars->q_full[b], 0, (int)(qt * NT));
+          ptx::bulk_load(qbuf + b * C::kQ + NT * KB, qs + qt * nkc * 512, nkc * 512, &bars->q_full[b]);
+          ++jq;
+        }
+        if (it >= C::kRaw && !ptx::mbar_wait(&bars->empty[s], ph, abort)) {
+          ok = false;
+          break;
+        }
+        const int64_t v0 = w.v() * C::kSub * kMxBM;
+        const int rows = (int)min((int64_t)C::kSub * kMxBM, n - v0);
+        const uint32_t bytes = (uint32_t)rows * nb * 16, sfb = (rows + 127) / 128 * nkc * 512;
+        unsigned char* to = raw + s * C::kTile;
+        ptx::mbar_arrive_expect_tx(&bars->full[s], bytes + sfb);
+        ptx::bulk_load(to, xc + v0 * nb * 16, bytes, &bars->full[s]);
+        ptx::bulk_load(to + C::kSub * kMxBM * KB, xs + v0 / kMxBM * nkc * 512, sfb, &bars->full[s]);
+        ++it;
+        if (++s == C::kRaw) s = 0, ph ^= 1;
+      }
+      if (!ok) mx_timeout(status, bars);
+      if (*abort) {  // let every copy this thread started land before the CTA exits
+        for (uint32_t k = (it > C::kRaw ? it - C::kRaw : 0); k < it; ++k)
+          ptx::mbar_drain(&bars->full[k % C::kRaw], (k / C::kRaw) & 1);
+        for (uint32_t k = (jq > 2 ? jq - 2 : 0); k < jq; ++k)
+          ptx::mbar_drain(&bars->q_full[k & 1], (k >> 1) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint64_t kHiK = KB == 128 ? ptx::sw128_hi(16, 1024) : ptx::sw64_hi(16, 512);
+      const int steps = (nb + 1) / 2;
+      uint32_t j = 0, jq = 0, buf = C::kBufs - 1, use = 1;   // buffer and parity of its phase
+      int64_t qt = -1;
+      bool ok = true;
+      for (MxWalk<false> w(vtiles, qtiles); ok && w.more() && !*abort; ++j) {
+        if (++buf == C::kBufs) buf = 0, use ^= 1;
+        // (the scale columns of the buffer's last step are free with its sums)
+        if (j >= C::kBufs && !ptx::mbar_wait(&bars->s_empty[buf], use ^ 1, abort)) ok = false;
+        if (!ok) break;
+        if (w.q() != qt) {
+          qt = w.q();
+          ok = ptx::mbar_wait(&bars->q_full[jq & 1], (jq >> 1) & 1, abort);
+          if (!ok) break;
+          const uint32_t sf = ptx::smem_u32(qbuf + (jq & 1) * C::kQ + NT * KB);
+          for (int h = 0; h < nkc; ++h)
+            ptx::tmem_cp_32x128(tmem + C::kSfQ + (jq & 1) * 4 * C::kAtoms + 4 * h, ptx::rows16_desc(sf + 512 * h));
+          ++jq;
+        }
+        const uint32_t sfq = tmem + C::kSfQ + ((jq - 1) & 1) * 4 * C::kAtoms;
+        ok = ptx::mbar_wait(&bars->swz_full[buf], use, abort);
+        if (!ok) break;
+        const uint64_t db = ptx::sw128_desc(ptx::smem_u32(qbuf + ((jq - 1) & 1) * C::kQ), kHiK);
+#pragma unroll
+        for (int u = 0; u < C::kSub; ++u) {
+          const uint32_t a = ptx::smem_u32(swz + buf * C::kTile + u * C::kOne), sf = a + kMxBM * KB;
+          const uint32_t sfa = tmem + C::kSfA + (buf * C::kSub + u) * 4 * C::kAtoms;
+          for (int h = 0; h < nkc; ++h)
+            ptx::tmem_cp_32x128(sfa + 4 * h, ptx::rows16_desc(sf + 512 * h));
+          const uint64_t da = ptx::sw128_desc(a, kHiK);
+#pragma unroll
+          for (int q = 0; q < 2 * C::kAtoms; ++q)
+            if (q < steps)
+              ptx::mma_mxf4_ss(tmem + (buf * C::kSub + u) * NT, da + 2 * q, db + 2 * q,
+                               ptx::idesc_mxf4(kMxBM, NT, 2 * (q & 1)), sfa + 4 * (q >> 1),
+                               sfq + 4 * (q >> 1), q > 0);
+        }
+        ptx::mma_commit(&bars->swz_empty[buf]);
+        ptx::mma_commit(&bars->s_full[buf]);
+        w.next();
+        if (w.more() && w.q() != qt) ptx::mma_commit(&bars->q_empty[(jq - 1) & 1]);
+      }
+      if (!ok) mx_timeout(status, bars);
+      if (*abort) {  // wait for the products already issued before TMEM is freed
+        ptx::mma_commit(&bars->drain);
+        ptx::mbar_drain(&bars->drain, 0);
+      }
+    }
+  } else if (warp < 4 || warp >= 4 + C::kWarps) {
+    // from the order of memory to the swizzled one: 16-byte chunk c of row r goes to chunk
+    // c ^ (r mod 8) of 128-byte rows, c ^ (r / 2 mod 4) of 64-byte rows
+    const int t = threadIdx.x - 64 - (warp < 4 ? 0 : 32 * C::kWarps);
+    constexpr int kMove = 32 * C::kMoveWarps;
+    const uint32_t inv = (65536u + nb - 1) / nb;     // i / nb for i < 2048
+    uint32_t s = 0, ph = 0, j = 0, buf = C::kBufs - 1, use = 1;
+    for (MxWalk<false> w(vtiles, qtiles); w.more(); w.next(), ++j) {
+      if (++buf == C::kBufs) buf = 0, use ^= 1;
+      bool ok = ptx::mbar_wait_warp(&bars->full[s], ph, abort);
+      if (ok && j >= C::kBufs) ok = ptx::mbar_wait_warp(&bars->swz_empty[buf], use ^ 1, abort);
+      if (!ok) {
         mx_timeout(status, bars);
         break;
       }
-      ptx::tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < kColsWarp; c += kChunk32) {
-        uint32_t u[kChunk32];
-        if constexpr (kChunk32 == 32) ptx::tmem_ld32(tmem + lane_base + buf * NT + c0 + c, u);
-        else ptx::tmem_ld16(tmem + lane_base + buf * NT + c0 + c, u);
-        ptx::tmem_wait_ld();
-        if (c + kChunk32 == kColsWarp) {  // all in registers: hand the accumulator back
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&bars->s_empty[buf]);
-        }
-        const int64_t mc = m0 + c0 + c;
-        T* p = out + mc * ldo + row;
-        if (row < n) {
-          if (mc + kChunk32 <= m) {
-#pragma unroll
-            for (int e = 0; e < kChunk32; ++e, p += ldo) mx_st(p, fmaf(alpha, __uint_as_float(u[e]), bv));
-          } else {
-#pragma unroll
-            for (int e = 0; e < kChunk32; ++e, p += ldo)
-              if (mc + e < m) mx_st(p, fmaf(alpha, __uint_as_float(u[e]), bv));
-          }
-        }
+      const uint4* from = reinterpret_cast<const uint4*>(raw + s * C::kTile);
+      uint4* to = reinterpret_cast<uint4*>(swz + buf * C::kTile);
+      const int rows = (int)min((int64_t)C::kSub * kMxBM, n - w.v() * C::kSub * kMxBM);
+#pragma unroll 4
+      for (int i = t; i < rows * nb; i += kMove) {
+        const uint32_t r = (uint32_t)i * inv >> 16, c = i - r * nb;
+        to[(r >> 7) * (C::kOne / 16) + (r & 127) * (KB / 16) + (c ^ (KB == 128 ? r & 7 : r >> 1 & 3))] =
+            from[i];
       }
+      for (int i = t; i < nkc * 32; i += kMove)
+#pragma unroll
+        for (int u = 0; u < C::kSub; ++u)
+          if (128 * u < rows)
+            to[u * (C::kOne / 16) + kMxBM * KB / 16 + i] =
+                from[C::kSub * kMxBM * KB / 16 + u * nkc * 32 + i];
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        ptx::mbar_arrive(&bars->swz_full[buf]);
+        ptx::mbar_arrive(&bars->empty[s]);
+      }
+      if (++s == C::kRaw) s = 0, ph ^= 1;
     }
+  } else {
+    mx_epilogue<NT, C::kSub, C::kBufs, false, T>(warp - 4, bars, outbuf, tmem, n, m, vtiles, qtiles, alpha, bias, out, ldo, status);
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -388,16 +758,19 @@ EncodeTiledFn mx_encode_tiled() {
   return fn;
 }
 
-// Rows of codes as boxes of 128 bytes x `box_rows`; what lies beyond a row or the last row is 0.
-bool mx_tmap(CUtensorMap* map, const uint8_t* codes, int nb, int64_t rows, int box_rows) {
+// Rows of codes as boxes of `box_bytes` (64 or 128, swizzled as wide) x `box_rows`; what lies beyond
+// a row or the last row is 0.
+bool mx_tmap(CUtensorMap* map, const uint8_t* codes, int nb, int64_t rows, int box_bytes,
+             int box_rows) {
   EncodeTiledFn enc = mx_encode_tiled();
   if (!enc) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)nb * 16, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)nb * 16};
-  const cuuint32_t box[2] = {kMxRowB, (cuuint32_t)box_rows};
+  const cuuint32_t box[2] = {(cuuint32_t)box_bytes, (cuuint32_t)box_rows};
   const cuuint32_t one[2] = {1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, box,
-             one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -413,39 +786,72 @@ struct MxArgs {
   cudaStream_t s;
 };
 
-template <int NT, typename T>
-cudaError_t mx_scores(const MxArgs& a) {
-  using C = MxCfg<NT>;
-  static_assert(C::kStages >= 4 && C::kStages <= 10 && C::kSfCol + 32 <= C::kCols, "tile");
-  constexpr int smem = 1024 + C::kStages * C::kStage + (int)sizeof(MxBars);
-  static_assert(smem <= 227 * 1024, "shared memory");
-  CUtensorMap tmx, tmq;
-  if (!mx_tmap(&tmx, a.xc, a.nb, a.n, kMxBM) || !mx_tmap(&tmq, a.qc, a.nb, a.m, NT))
-    return cudaErrorInvalidValue;
-  auto* k = mx4_scores_kernel<NT, T>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+// Grid and attributes of a kernel with configuration C; its query and vector tiles.
+template <typename C, typename K>
+cudaError_t mx_grid_of(K* kernel, int64_t tiles, unsigned* grid) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   int dev = 0, sms = 0;
   if (e == cudaSuccess) e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
-  const int64_t mt = (a.m + NT - 1) / NT, tiles = (a.n + kMxBM - 1) / kMxBM * mt;
-  k<<<(unsigned)(tiles < sms ? tiles : sms), C::kThreads, smem, a.s>>>(
-      tmx, tmq, a.xs, a.qs, a.n, a.m, a.nb, tiles, (int)mt, a.alpha, a.bias, static_cast<T*>(a.out),
-      a.ldo, a.status);
+  const int64_t slots = (int64_t)sms * C::kCtas;
+  *grid = (unsigned)(tiles < slots ? tiles : slots);
+  return e;
+}
+
+template <int NT, int KB, typename T>
+cudaError_t mx_scores(const MxArgs& a) {
+  const int64_t qt = (a.m + NT - 1) / NT, vt = (a.n + kMxBM - 1) / kMxBM;
+  unsigned grid = 0;
+  CUtensorMap tmx, tmq;
+  cudaError_t e;
+  if (!mx_tmap(&tmq, a.qc, a.nb, a.m, KB, NT)) return cudaErrorInvalidValue;
+  // Bulk copies for rows shorter than a box.  Rows that fill one (128 and 256 dimensions) are moved
+  // by TMA at the rate of memory, and where the codes are most of the traffic the shorter way gains
+  // (one query and 10^6 vectors: 17.6 us against 21.9 at 128 dimensions, 29.4 against 35.2 at 256);
+  // where the output is, TMA is left to the stores (16 queries of 10^6 x 128: 33.2 us by boxes, 24.7;
+  // 1000 x 100003 x 256: 106, 92).
+  constexpr bool kBoxes = KB == 128 || NT < 128;    // (128 queries write more than they read there)
+  const bool full = 16 * a.nb == KB && 2 * a.m * (int64_t)sizeof(T) <= 17 * a.nb;
+  if (!kBoxes || (16 * a.nb <= KB && !full)) {
+    using C = MxPackCfg<NT, KB>;
+    const int64_t steps = (vt + C::kSub - 1) / C::kSub;
+    auto* k = mx4_scores_packed_kernel<NT, KB, T>;
+    if ((e = mx_grid_of<C>(k, steps * qt, &grid)) != cudaSuccess) return e;
+    k<<<grid, C::kThreads, C::kSmem, a.s>>>(tmq, a.xc, a.xs, a.qs, a.n, a.m, a.nb, steps, qt, a.alpha, a.bias,
+                                            static_cast<T*>(a.out), a.ldo, a.status);
+    return cudaGetLastError();
+  }
+  if constexpr (kBoxes) {
+    using C = MxCfg<NT, KB>;
+    auto* k = mx4_scores_kernel<NT, KB, T>;
+    if ((e = mx_grid_of<C>(k, vt * qt, &grid)) != cudaSuccess) return e;
+    if (!mx_tmap(&tmx, a.xc, a.nb, a.n, KB, kMxBM)) return cudaErrorInvalidValue;
+    k<<<grid, C::kThreads, C::kSmem, a.s>>>(tmx, tmq, a.xs, a.qs, a.n, a.m, a.nb, vt, qt, a.alpha, a.bias,
+                                            static_cast<T*>(a.out), a.ldo, a.status);
+  }
   return cudaGetLastError();
 }
 
-template <typename T>
+template <int KB, typename T>
 cudaError_t mx_scores_nt(const MxArgs& a) {
-  if (a.m <= 16) return mx_scores<16, T>(a);
-  if (a.m <= 32) return mx_scores<32, T>(a);
-  if (a.m <= 64) return mx_scores<64, T>(a);
-  return mx_scores<128, T>(a);
+  if (a.m <= 16) return mx_scores<16, KB, T>(a);
+  if (a.m <= 32) return mx_scores<32, KB, T>(a);
+  if (a.m <= 64) return mx_scores<64, KB, T>(a);
+  return mx_scores<128, KB, T>(a);
+}
+template <typename T>
+cudaError_t mx_scores_kb(const MxArgs& a) {
+  return a.nb <= 4 ? mx_scores_nt<64, T>(a) : mx_scores_nt<128, T>(a);
 }
 
-unsigned mx_grid(int64_t groups) {
-  const int64_t blocks = (groups + kMxThreads / 32 - 1) / (kMxThreads / 32);
-  return (unsigned)(blocks < (1 << 30) ? blocks : (1 << 30));
+// Blocks for `pieces` threads' worth of work: enough to fill the device, fewer when there is less.
+cudaError_t mx_blocks(int64_t pieces, unsigned* grid) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int64_t need = (pieces + kMxThreads - 1) / kMxThreads, most = (int64_t)sms * 16;
+  *grid = (unsigned)(need < most ? need : most);
+  return e;
 }
 
 }  // namespace
@@ -454,18 +860,18 @@ unsigned mx_grid(int64_t groups) {
 cudaError_t launch_mx4_encode(const void* X, int x_dtype, int64_t n, int D, int64_t ldx,
                               uint8_t* codes, uint8_t* scales, cudaStream_t s) {
   const int nb = (D + 31) / 32, nkc = (nb + 3) / 4;
-  const int64_t groups = (n + 127) / 128 * 32 * nkc;
-  const unsigned grid = mx_grid(groups);
-  const size_t eb = x_dtype == FGMM_F32 ? 4 : 2;
-  const bool vec = (uintptr_t)X % (4 * eb) == 0 && ldx % 4 == 0;
+  const int eb = x_dtype == FGMM_F32 ? 4 : 2;
+  const bool vec = (uintptr_t)X % 16 == 0 && ldx * eb % 16 == 0;
+  unsigned grid = 0;
+  cudaError_t e = mx_blocks((n + 127) / 128 * 128 * nb * eb, &grid);
+  if (e != cudaSuccess) return e;
   if (x_dtype == FGMM_F32) {
     auto* k = vec ? mx4_encode_kernel<float, true> : mx4_encode_kernel<float, false>;
-    k<<<grid, kMxThreads, 0, s>>>(static_cast<const float*>(X), n, D, ldx, nb, nkc, groups, codes,
-                                  scales);
+    k<<<grid, kMxThreads, 0, s>>>(static_cast<const float*>(X), n, D, ldx, nb, nkc, codes, scales);
   } else {
     auto* k = vec ? mx4_encode_kernel<__nv_bfloat16, true> : mx4_encode_kernel<__nv_bfloat16, false>;
-    k<<<grid, kMxThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(X), n, D, ldx, nb, nkc, groups,
-                                  codes, scales);
+    k<<<grid, kMxThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(X), n, D, ldx, nb, nkc, codes,
+                                  scales);
   }
   return cudaGetLastError();
 }
@@ -473,17 +879,17 @@ cudaError_t launch_mx4_encode(const void* X, int x_dtype, int64_t n, int D, int6
 cudaError_t launch_mx4_decode(const uint8_t* codes, const uint8_t* scales, int64_t n, int D,
                               void* out, int out_dtype, int64_t ldo, cudaStream_t s) {
   const int nb = (D + 31) / 32, nkc = (nb + 3) / 4;
-  const int64_t groups = (n + 127) / 128 * 32 * nkc;
-  const unsigned grid = mx_grid(groups);
-  const size_t eb = out_dtype == FGMM_F32 ? 4 : 2;
-  const bool vec = (uintptr_t)out % (4 * eb) == 0 && ldo % 4 == 0;
+  const int eb = out_dtype == FGMM_F32 ? 4 : 2;
+  const bool vec = (uintptr_t)out % 16 == 0 && ldo * eb % 16 == 0;
+  const int nkg = (D * eb + 511) / 512;             // 512-byte pieces of a row
+  const int64_t groups = (n + 127) / 128 * 32 * nkg, blocks = (groups + kMxThreads / 32 - 1) / (kMxThreads / 32);
+  const unsigned grid = (unsigned)(blocks < (1 << 30) ? blocks : (1 << 30));
   if (out_dtype == FGMM_F32) {
     auto* k = vec ? mx4_decode_kernel<float, true> : mx4_decode_kernel<float, false>;
-    k<<<grid, kMxThreads, 0, s>>>(codes, scales, n, D, nb, nkc, groups, static_cast<float*>(out),
-                                  ldo);
+    k<<<grid, kMxThreads, 0, s>>>(codes, scales, n, D, nb, nkc, nkg, groups, static_cast<float*>(out), ldo);
   } else {
     auto* k = vec ? mx4_decode_kernel<__nv_bfloat16, true> : mx4_decode_kernel<__nv_bfloat16, false>;
-    k<<<grid, kMxThreads, 0, s>>>(codes, scales, n, D, nb, nkc, groups,
+    k<<<grid, kMxThreads, 0, s>>>(codes, scales, n, D, nb, nkc, nkg, groups,
                                   static_cast<__nv_bfloat16*>(out), ldo);
   }
   return cudaGetLastError();
@@ -495,7 +901,7 @@ cudaError_t launch_mx4_scores(const uint8_t* q_codes, const uint8_t* q_scales, i
                               int64_t ldo, int* status, cudaStream_t s) {
   const MxArgs a = {q_codes, q_scales, codes, scales, m, n, (D + 31) / 32, alpha, bias, out, ldo,
                     status, s};
-  return out_dtype == FGMM_F32 ? mx_scores_nt<float>(a) : mx_scores_nt<__nv_bfloat16>(a);
+  return out_dtype == FGMM_F32 ? mx_scores_kb<float>(a) : mx_scores_kb<__nv_bfloat16>(a);
 }
 
 }  // namespace fgmm

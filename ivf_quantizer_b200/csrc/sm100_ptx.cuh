@@ -120,6 +120,22 @@ __device__ __forceinline__ void bulk_load(void* smem_dst, const void* gsrc, uint
       : "memory");
 }
 
+// Untiled bulk copy shared -> global (16-byte aligned addresses, size a multiple of 16), in the
+// thread's current bulk group.
+__device__ __forceinline__ void bulk_store(void* gdst, uint32_t ssrc, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(gdst), "r"(ssrc),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Until at most N of the thread's bulk groups still read their shared memory.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
 // Bulk prefetch of global memory into L2 (16-byte aligned address, size a multiple of 16).
 __device__ __forceinline__ void bulk_prefetch_l2(const void* gsrc, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(gsrc), "r"(bytes) : "memory");
@@ -283,6 +299,29 @@ __host__ __device__ constexpr uint64_t sw128_hi(uint32_t lbo_bytes, uint32_t sbo
 }
 __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint64_t hi) {
   return hi | (uint64_t)((saddr >> 4) & 0x3FFFu);
+}
+
+// The same for 64-byte-swizzled tiles (rows of 64 bytes, 8-row atoms of 512).
+__host__ __device__ constexpr uint64_t sw64_hi(uint32_t lbo_bytes, uint32_t sbo_bytes) {
+  return ((uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)((sbo_bytes >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) |
+         ((uint64_t)4 << 61);
+}
+
+// Barrier of `threads` threads of the CTA (whole warps), id 1 .. 15.
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// The same, telling every thread whether `ok` held on all of them.
+__device__ __forceinline__ bool named_all(int id, int threads, bool ok) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %3, 0;\n\tbar.red.and.pred q, %1, %2, p;\n\t"
+      "selp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"((int)ok)
+      : "memory");
+  return r != 0;
 }
 
 // ------------------------------------------------------------------ packed fp32 and exp2
