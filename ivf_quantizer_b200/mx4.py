@@ -12,21 +12,34 @@ from ._lib import LIB, check
 _DTYPES = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16}
 
 
-def on_device(t: torch.Tensor):
-    """(guard, stream) for a call on t's device: the guard makes it the current one."""
-    return torch.cuda.device(t.device), torch.cuda.current_stream(t.device).cuda_stream
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def call(fn, name: str, device: torch.device, *args) -> None:
+    """fn(*args, current stream of `device`) with `device` as the current one."""
+    i = device.index
+    if i == torch.cuda.current_device():
+        code = fn(*args, _raw_stream(i))
+    else:
+        with torch.cuda.device(i):
+            code = fn(*args, _raw_stream(i))
+    if code:
+        check(code, name)
 
 
 def _rows(X: torch.Tensor, what: str):
+    """(dtype code, rows, columns, row stride) of a 2-D tensor with contiguous rows."""
     if not (isinstance(X, torch.Tensor) and X.is_cuda and X.dim() == 2):
         raise ValueError(f"{what} must be a 2-D CUDA tensor")
-    if X.dtype not in _DTYPES:
+    dt = _DTYPES.get(X.dtype)
+    if dt is None:
         raise TypeError(f"{what} must be float32 or bfloat16")
-    if X.shape[1] < 1:
+    (n, d), (ld, one) = X.shape, X.stride()
+    if d < 1:
         raise ValueError(f"{what} must have at least one dimension")
-    if X.shape[1] > 1 and X.stride(1) != 1 or X.shape[0] > 1 and X.stride(0) < X.shape[1]:
+    if d > 1 and one != 1 or n > 1 and ld < d:
         raise ValueError(f"{what} rows must be contiguous and must not overlap")
-    return _DTYPES[X.dtype], max(X.stride(0), X.shape[1])
+    return dt, n, d, max(ld, d)
 
 
 class MX4:
@@ -37,20 +50,13 @@ class MX4:
     """
 
     def __init__(self, X: torch.Tensor):
-        dt, ldx = _rows(X, "X")
-        N, D = X.shape
+        dt, N, D, ldx = _rows(X, "X")
+        dev, nb = X.device, -(-D // _lib.MX4_BLOCK)
         self.shape = (N, D)
-        self.codes, self.scales = self._empty(N, D, X.device)
-        guard, stream = on_device(X)
-        with guard:
-            check(LIB.fgmm_mx4_encode(X.data_ptr(), dt, N, D, ldx, self.codes.data_ptr(),
-                                      self.scales.data_ptr(), stream), "fgmm_mx4_encode")
-
-    @staticmethod
-    def _empty(N, D, device):
-        nb = -(-D // _lib.MX4_BLOCK)
-        return (torch.empty(N, nb * 16, dtype=torch.uint8, device=device),
-                torch.empty(-(-N // 128) * -(-nb // 4) * 512, dtype=torch.uint8, device=device))
+        self.codes = torch.empty((N, nb * 16), dtype=torch.uint8, device=dev)
+        self.scales = torch.empty(-(-N // 128) * -(-nb // 4) * 512, dtype=torch.uint8, device=dev)
+        call(LIB.fgmm_mx4_encode, "fgmm_mx4_encode", dev, X.data_ptr(), dt, N, D, ldx,
+             self.codes.data_ptr(), self.scales.data_ptr())
 
     @classmethod
     def from_codes(cls, codes: torch.Tensor, scales: torch.Tensor, D: int) -> "MX4":
@@ -75,11 +81,10 @@ class MX4:
         if dtype not in _DTYPES:
             raise TypeError("dtype must be float32 or bfloat16")
         N, D = self.shape
-        out = torch.empty(N, D, dtype=dtype, device=self.codes.device)
-        guard, stream = on_device(out)
-        with guard:
-            check(LIB.fgmm_mx4_decode(self.codes.data_ptr(), self.scales.data_ptr(), N, D,
-                                      out.data_ptr(), _DTYPES[dtype], D, stream), "fgmm_mx4_decode")
+        dev = self.codes.device
+        out = torch.empty((N, D), dtype=dtype, device=dev)
+        call(LIB.fgmm_mx4_decode, "fgmm_mx4_decode", dev, self.codes.data_ptr(),
+             self.scales.data_ptr(), N, D, out.data_ptr(), _DTYPES[dtype], D)
         return out
 
     def scores(self, queries, alpha: float = 1.0, bias: torch.Tensor | None = None,
@@ -98,11 +103,8 @@ class MX4:
         if bias is not None and not (bias.device == dev and bias.dtype == torch.float32
                                      and bias.shape == (N,) and bias.is_contiguous()):
             raise ValueError("bias must be a contiguous float32 [N] tensor on the codes' device")
-        out = torch.empty(M, N, dtype=dtype, device=dev)
-        guard, stream = on_device(out)
-        with guard:
-            check(LIB.fgmm_mx4_scores(q.codes.data_ptr(), q.scales.data_ptr(), M,
-                                      self.codes.data_ptr(), self.scales.data_ptr(), N, D, alpha,
-                                      None if bias is None else bias.data_ptr(), out.data_ptr(),
-                                      _DTYPES[dtype], N, None, stream), "fgmm_mx4_scores")
+        out = torch.empty((M, N), dtype=dtype, device=dev)
+        call(LIB.fgmm_mx4_scores, "fgmm_mx4_scores", dev, q.codes.data_ptr(), q.scales.data_ptr(), M,
+             self.codes.data_ptr(), self.scales.data_ptr(), N, D, alpha,
+             None if bias is None else bias.data_ptr(), out.data_ptr(), _DTYPES[dtype], N, None)
         return out

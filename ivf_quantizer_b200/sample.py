@@ -4,8 +4,8 @@ from __future__ import annotations
 
 import torch
 
-from ._lib import LIB, check
-from .mx4 import _rows, on_device
+from ._lib import LIB
+from .mx4 import _rows, call
 
 
 def _per_row(v, name, dtype, rows, device):
@@ -32,22 +32,18 @@ def sample_logits(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k
     index was drawn.  A row without a finite logit gives -1 and 0; one with a NaN or with a
     parameter outside its range gives -1 and NaN.
     """
-    dt, ld = _rows(logits, "logits")
-    rows, V = logits.shape
+    dt, rows, V, ld = _rows(logits, "logits")
     dev = logits.device
     if u is None:
         raise ValueError("u must be a float64 [rows] tensor")
-    guard, stream = on_device(logits)
-    with guard:
-        u = _per_row(u, "u", torch.float64, rows, dev)
-        temperature = _per_row(temperature, "temperature", torch.float32, rows, dev)
-        top_k = _per_row(top_k, "top_k", torch.int32, rows, dev)
-        top_p = _per_row(top_p, "top_p", torch.float32, rows, dev)
-        min_p = _per_row(min_p, "min_p", torch.float32, rows, dev)
-        ids = torch.empty(rows, dtype=torch.int32, device=dev)
-        prob = torch.empty(rows, dtype=torch.float32, device=dev)
-        check(LIB.fgmm_sample_logits(
-            logits.data_ptr(), dt, rows, V, ld,
-            *(None if t is None else t.data_ptr() for t in (temperature, top_k, top_p, min_p)),
-            u.data_ptr(), ids.data_ptr(), prob.data_ptr(), stream), "fgmm_sample_logits")
+    u = _per_row(u, "u", torch.float64, rows, dev)
+    temperature = _per_row(temperature, "temperature", torch.float32, rows, dev)
+    top_k = _per_row(top_k, "top_k", torch.int32, rows, dev)
+    top_p = _per_row(top_p, "top_p", torch.float32, rows, dev)
+    min_p = _per_row(min_p, "min_p", torch.float32, rows, dev)
+    ids = torch.empty(rows, dtype=torch.int32, device=dev)
+    prob = torch.empty(rows, dtype=torch.float32, device=dev)
+    call(LIB.fgmm_sample_logits, "fgmm_sample_logits", dev, logits.data_ptr(), dt, rows, V, ld,
+         *[None if t is None else t.data_ptr() for t in (temperature, top_k, top_p, min_p)],
+         u.data_ptr(), ids.data_ptr(), prob.data_ptr())
     return ids, prob
