@@ -336,6 +336,28 @@ struct MxWalk {
 __device__ __forceinline__ void mx_cvt(float v, float& o) { o = v; }
 __device__ __forceinline__ void mx_cvt(float v, __nv_bfloat16& o) { o = __float2bfloat16_rn(v); }
 
+// 16 staged queries leave as bulk copies: four a warp, eight lanes each.  One lane copies the aligned
+// inside of a query's `len` scores, all write what lies before and behind it.  Element (query r,
+// vector i) lies at st[r][phase_r + i], phase_r = (p0 + r dp) mod VN being what its address is off a
+// 16-byte boundary; `out` is that of (query 0, vector 0).
+template <typename T>
+__device__ __forceinline__ void mx_rows_out(unsigned char* st, int row_bytes, int q, int lane, int rows,
+                                            int len, int p0, int dp, T* out, int64_t ldo) {
+  constexpr int VN = 16 / sizeof(T);
+  const int r = 4 * q + (lane >> 3), ph = (p0 + r * dp) & (VN - 1), end = ph + len;
+  const int a0 = (ph + VN - 1) & ~(VN - 1), a1 = end & ~(VN - 1);
+  if (r < rows) {
+    const T* from = reinterpret_cast<const T*>(st + r * row_bytes);
+    T* to = out + r * ldo - ph;
+    if ((lane & 7) == 0 && a1 > a0)
+      ptx::bulk_store(to + a0, ptx::smem_u32(from + a0), (uint32_t)(a1 - a0) * sizeof(T));
+    const int i = lane & 7;
+    if (i >= ph && i < min(a0, end)) to[i] = from[i];
+    if (max(a0, a1) + i < end) to[max(a0, a1) + i] = from[max(a0, a1) + i];
+  }
+  ptx::bulk_commit();
+}
+
 // The epilogue warps (`warp` from 0, a multiple of 4 in the CTA) of a CTA: scale, bias, rounding and
 // the stores of every step of SUB vector tiles.
 template <int NT, int SUB, int BUFS, bool QFAST, typename T>
@@ -400,21 +422,8 @@ __device__ __forceinline__ void mx_epilogue(int warp, MxBars* bars, unsigned cha
                  mine[e * (C::kOutRow / sizeof(T)) + ((p0 + e * dp) & (VN - 1))]);
         ptx::fence_proxy_async_smem();
         ptx::named_sync(1 + grp, 128);
-        // four queries a warp, eight lanes each: one copies the aligned inside of the row, all
-        // write what lies before and behind it
-        const int r = 4 * q + (lane >> 3), ph = (p0 + r * dp) & (VN - 1);
-        const int end = ph + (int)min((int64_t)kMxBM, n - n0);
-        const int a0 = (ph + VN - 1) & ~(VN - 1), a1 = end & ~(VN - 1);
-        if (r < rows) {
-          const T* from = reinterpret_cast<const T*>(st + r * C::kOutRow);
-          T* to = out + (mc + r) * ldo + n0 - ph;
-          if ((lane & 7) == 0 && a1 > a0)
-            ptx::bulk_store(to + a0, ptx::smem_u32(from + a0), (uint32_t)(a1 - a0) * sizeof(T));
-          const int i = lane & 7;
-          if (i >= ph && i < min(a0, end)) to[i] = from[i];
-          if (max(a0, a1) + i < end) to[max(a0, a1) + i] = from[max(a0, a1) + i];
-        }
-        ptx::bulk_commit();
+        mx_rows_out<T>(st, C::kOutRow, q, lane, rows, (int)max((int64_t)0, min((int64_t)kMxBM, n - n0)), p0,
+                       dp, out + mc * ldo + n0, ldo);
       } else if (row < n) {
         T* o = out + mc * ldo + row;
 #pragma unroll
@@ -742,6 +751,237 @@ __global__ void __launch_bounds__(MxPackCfg<NT, KB>::kThreads, MxPackCfg<NT, KB>
   }
 }
 
+// ------------------------------------------------------------------ scores by pairs of CTAs
+// Many queries of long vectors: the products decide, and what bounds them is how fast operands come
+// into shared memory (TMA moves about 30 bytes a clock and SM).  A pair of CTAs shares a tile of 256
+// vectors x 256 queries: each loads its 128 vectors and half of the queries, 32 KB for 128 x 256 x 256
+// products, half of what a tile of 128 x 128 needs.  The first CTA's thread issues the products of both;
+// a thread of the second passes on that its stage is full.
+//
+// Two accumulators of 256 columns and the scales do not fit into 512 columns, so the accumulators
+// overlap by 32: the epilogue drains those first, and the next tile's products wait for them alone.
+template <typename T>
+struct MxPairCfg {
+  static constexpr int NT = 256, KB = 128, kAtoms = 2;
+  static constexpr int kA = kMxBM * KB, kB = NT / 2 * KB, kSf = 1024;
+  static constexpr int kStage = kA + kB + 3 * kSf;  // own vectors, half of the queries; scales: own, all
+  static constexpr int kGroups = 4, kWarps = 4 * kGroups, kThreads = 128 + 32 * kWarps;
+  static constexpr int kOutRow = 128 * sizeof(T) + 16;
+  static constexpr int kOut = kGroups * 2 * 16 * kOutRow;
+  static constexpr int kBudget = 226 * 1024 - 1024 - 512 - kOut;
+  static constexpr int kStages = kBudget / kStage < kMxMaxStages ? kBudget / kStage : kMxMaxStages;
+  static constexpr int kSmem = 1024 + kStages * kStage + kOut + 512;
+  static constexpr int kOverlap = 32, kAcc1 = NT - kOverlap, kSfCol = 2 * NT - kOverlap;
+  static_assert(kStages >= 3 && kSfCol + 2 * 12 <= 512, "tile");
+};
+
+struct MxPairBars {
+  uint64_t full[kMxMaxStages], peer[kMxMaxStages], empty[kMxMaxStages];
+  uint64_t s_full[2], s_empty[2], overlap, drain;
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(MxPairBars) <= 512, "barriers");
+
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxPairCfg<T>::kThreads, 1)
+    mx4_scores_pair_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmq,
+                           const uint8_t* __restrict__ xs, const uint8_t* __restrict__ qs, int64_t n,
+                           int64_t m, int nb, int64_t vpairs, int64_t qtiles, float alpha,
+                           const float* __restrict__ bias, T* __restrict__ out, int64_t ldo, int* status) {
+  using C = MxPairCfg<T>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* ring = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  unsigned char* outbuf = ring + C::kStages * C::kStage;
+  MxPairBars* bars = reinterpret_cast<MxPairBars*>(outbuf + C::kOut);
+  volatile int* abort = &bars->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = blockIdx.x & 1;
+  const int nkc = (nb + 3) / 4, nst = (nkc + 1) / 2;
+  const int64_t vtiles = (n + kMxBM - 1) / kMxBM, qsf_tiles = (m + kMxBM - 1) / kMxBM;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      ptx::mbar_init(&bars->full[s], 1);
+      ptx::mbar_init(&bars->peer[s], 1);
+      ptx::mbar_init(&bars->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(&bars->s_full[b], 1);
+      ptx::mbar_init(&bars->s_empty[b], 2 * C::kWarps);
+    }
+    ptx::mbar_init(&bars->overlap, 2 * 4);
+    ptx::mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(&bars->tmem, 512);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+  auto timeout = [&] {
+    if (status) atomicCAS(status, FGMM_OK, FGMM_ERR_TIMEOUT);
+    bars->abort = 1;
+  };
+  // tiles of the pair, queries fastest
+  const int64_t p0 = blockIdx.x >> 1, np = gridDim.x >> 1, ntiles = vpairs * qtiles;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      ptx::prefetch_tmap(&tmx);
+      ptx::prefetch_tmap(&tmq);
+      uint32_t it = 0, s = 0, ph = 1;
+      bool ok = true;
+      for (int64_t t = p0; ok && t < ntiles && !*abort; t += np) {
+        const int64_t vp = t / qtiles, qt = t - vp * qtiles;
+        const int64_t vt = 2 * vp + rank;           // (may be behind the last tile: zeros then)
+        for (int k = 0; k < nst; ++k) {
+          if (it >= C::kStages && !ptx::mbar_wait(&bars->empty[s], ph, abort)) {
+            timeout();
+            ok = false;
+            break;
+          }
+          unsigned char* a = ring + s * C::kStage;
+          unsigned char* sf = a + C::kA + C::kB;
+          const uint32_t sfb = min(nkc - 2 * k, 2) * 512;
+          const bool second = 2 * qt + 1 < qsf_tiles;
+          const int64_t vsf = vt < vtiles ? vt : vtiles - 1;   // scales of what is not there: any
+          ptx::mbar_arrive_expect_tx(&bars->full[s], C::kA + C::kB + (second ? 3 : 2) * sfb);
+          ptx::tma_load_2d(a, &tmx, &bars->full[s], k * C::KB, (int)(vt * kMxBM));
+          ptx::tma_load_2d(a + C::kA, &tmq, &bars->full[s], k * C::KB, (int)(qt * C::NT + rank * (C::NT / 2)));
+          ptx::bulk_load(sf, xs + (vsf * nkc + 2 * k) * 512, sfb, &bars->full[s]);
+          ptx::bulk_load(sf + C::kSf, qs + (2 * qt * nkc + 2 * k) * 512, sfb, &bars->full[s]);
+          if (second)
+            ptx::bulk_load(sf + 2 * C::kSf, qs + ((2 * qt + 1) * nkc + 2 * k) * 512, sfb, &bars->full[s]);
+          ++it;
+          if (++s == C::kStages) s = 0, ph ^= 1;
+        }
+      }
+      if (*abort)  // let every copy this thread started land before the CTA exits
+        for (uint32_t k = (it > C::kStages ? it - C::kStages : 0); k < it; ++k)
+          ptx::mbar_drain(&bars->full[k % C::kStages], (k / C::kStages) & 1);
+    }
+  } else if (warp == 1 && rank == 1) {
+    if (lane == 0) {
+      uint32_t s = 0, ph = 0;
+      bool ok = true;
+      for (int64_t t = p0; ok && t < ntiles && !*abort; t += np)
+        for (int k = 0; k < nst; ++k) {
+          if (!ptx::mbar_wait(&bars->full[s], ph, abort)) {
+            timeout();
+            ok = false;
+            break;
+          }
+          ptx::mbar_arrive_cluster(&bars->peer[s], 0);
+          if (++s == C::kStages) s = 0, ph ^= 1;
+        }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint64_t kHiK = ptx::sw128_hi(16, 1024);
+      uint32_t s = 0, ph = 0, j = 0, cp = 0;
+      bool ok = true;
+      for (int64_t t = p0; ok && t < ntiles && !*abort; t += np, ++j) {
+        const uint32_t buf = j & 1;
+        if (j >= 2 && !ptx::mbar_wait_cluster(&bars->s_empty[buf], ((j >> 1) - 1) & 1, abort)) ok = false;
+        if (ok && j >= 1 && !ptx::mbar_wait_cluster(&bars->overlap, (j - 1) & 1, abort)) ok = false;
+        if (!ok) break;
+        const uint32_t d_tmem = tmem + (buf ? C::kAcc1 : 0);
+        for (int k = 0; k < nst; ++k) {
+          ok = ptx::mbar_wait(&bars->full[s], ph, abort) && ptx::mbar_wait_cluster(&bars->peer[s], ph, abort);
+          if (!ok) break;
+          const uint32_t a = ptx::smem_u32(ring + s * C::kStage), sf = a + C::kA + C::kB;
+          const uint64_t da = ptx::sw128_desc(a, kHiK), db = ptx::sw128_desc(a + C::kA, kHiK);
+          const int steps = min(4, (nb + 1) / 2 - 4 * k);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (2 * h < steps) {
+              // 12 columns of scales for 128 dimensions: the vectors' 4, the queries' 8
+              const uint32_t sft = tmem + C::kSfCol + (cp++ & 1) * 12;
+              ptx::tmem_cp_32x128_pair(sft, ptx::rows16_desc(sf + 512 * h));
+              ptx::tmem_cp_32x128_pair(sft + 4, ptx::rows16_desc(sf + C::kSf + 512 * h));
+              ptx::tmem_cp_32x128_pair(sft + 8, ptx::rows16_desc(sf + 2 * C::kSf + 512 * h));
+#pragma unroll
+              for (int q = 2 * h; q < 2 * h + 2; ++q)
+                if (q < steps)
+                  ptx::mma_mxf4_pair(d_tmem, da + 2 * q, db + 2 * q, ptx::idesc_mxf4(256, C::NT, 2 * (q & 1)),
+                                     sft, sft + 4, k > 0 || q > 0);
+            }
+          ptx::mma_commit_pair(&bars->empty[s]);
+          if (++s == C::kStages) s = 0, ph ^= 1;
+        }
+        if (ok) ptx::mma_commit_pair(&bars->s_full[buf]);
+      }
+      if (!ok) timeout();
+      if (*abort) {  // wait for the products already issued before TMEM is freed
+        ptx::mma_commit_pair(&bars->drain);
+        ptx::mbar_drain(&bars->drain, 0);
+      }
+    }
+  } else if (warp >= 4) {
+    constexpr int VN = 16 / sizeof(T);
+    const int q = warp & 3, grp = (warp - 4) >> 2;
+    uint32_t j = 0;
+    for (int64_t t = p0; t < ntiles; t += np, ++j) {
+      const int64_t vp = t / qtiles, qt = t - vp * qtiles;
+      const uint32_t buf = j & 1;
+      const int64_t n0 = (2 * vp + rank) * kMxBM, row = n0 + q * 32 + lane;
+      const float bv = bias && row < n ? __ldg(bias + row) : 0.f;
+      bool ok = ptx::mbar_wait_warp(&bars->s_full[buf], (j >> 1) & 1, abort);
+      if (!ok) timeout();
+      ok = ptx::named_all(1 + grp, 128, ok);        // the four warps of a group go on or give up together
+      if (!ok) break;
+      ptx::tc_fence_after();
+      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (buf ? C::kAcc1 : 0) + grp * 64;
+      const int len = (int)max((int64_t)0, min((int64_t)kMxBM, n - n0));
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        const int c = 16 * (buf ? i : 3 - i);       // the shared columns first
+        uint32_t u[16];
+        ptx::tmem_ld16(acc + c, u);
+        ptx::tmem_wait_ld();
+        if (i == 1 && grp == (buf ? 0 : C::kGroups - 1)) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_cluster(&bars->overlap, 0);
+        }
+        if (i == 3) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_cluster(&bars->s_empty[buf], 0);
+        }
+        const int64_t mc = qt * C::NT + grp * 64 + c;
+        const int rows = (int)min((int64_t)16, m - mc);
+        unsigned char* st = outbuf + (grp * 2 + (i & 1)) * 16 * C::kOutRow;
+        const int pm = (int)(((uintptr_t)out / sizeof(T) + (uintptr_t)mc * ldo + n0) % VN), dp = (int)(ldo % VN);
+        ptx::bulk_wait_read<1>();
+        ptx::named_sync(1 + grp, 128);
+        T* mine = reinterpret_cast<T*>(st) + q * 32 + lane;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          mx_cvt(fmaf(alpha, __uint_as_float(u[e]), bv),
+                 mine[e * (C::kOutRow / sizeof(T)) + ((pm + e * dp) & (VN - 1))]);
+        ptx::fence_proxy_async_smem();
+        ptx::named_sync(1 + grp, 128);
+        mx_rows_out<T>(st, C::kOutRow, q, lane, rows, len, pm, dp, out + mc * ldo + n0, ldo);
+      }
+    }
+    ptx::bulk_wait_read<0>();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();                              // the other CTA's products read this one's memory
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem, 512);
+  }
+}
+
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -832,8 +1072,28 @@ cudaError_t mx_scores(const MxArgs& a) {
   return cudaGetLastError();
 }
 
+template <typename T>
+cudaError_t mx_scores_pair(const MxArgs& a) {
+  using C = MxPairCfg<T>;
+  CUtensorMap tmx, tmq;
+  if (!mx_tmap(&tmx, a.xc, a.nb, a.n, C::KB, kMxBM) || !mx_tmap(&tmq, a.qc, a.nb, a.m, C::KB, C::NT / 2))
+    return cudaErrorInvalidValue;
+  auto* k = mx4_scores_pair_kernel<T>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  int dev = 0, sms = 0;
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int64_t vp = (a.n + 2 * kMxBM - 1) / (2 * kMxBM), qt = (a.m + C::NT - 1) / C::NT;
+  const int64_t pairs = vp * qt < sms / 2 ? vp * qt : sms / 2;
+  k<<<(unsigned)(2 * pairs), C::kThreads, C::kSmem, a.s>>>(tmx, tmq, a.xs, a.qs, a.n, a.m, a.nb, vp, qt, a.alpha,
+                                                           a.bias, static_cast<T*>(a.out), a.ldo, a.status);
+  return cudaGetLastError();
+}
+
 template <int KB, typename T>
 cudaError_t mx_scores_nt(const MxArgs& a) {
+  if (KB == 128 && a.nb > 8 && a.m > 128 && a.n > 128) return mx_scores_pair<T>(a);
   if (a.m <= 16) return mx_scores<16, KB, T>(a);
   if (a.m <= 32) return mx_scores<32, KB, T>(a);
   if (a.m <= 64) return mx_scores<64, KB, T>(a);
