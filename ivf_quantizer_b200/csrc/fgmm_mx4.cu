@@ -382,7 +382,7 @@ __device__ __forceinline__ void mx_epilogue(int warp, MxBars* bars, unsigned cha
       const int64_t row = (w.v() * SUB + u) * kMxBM + q * 32 + lane;
       bvs[u] = bias && row < n ? __ldg(bias + row) : 0.f;
     }
-    bool ok = ptx::mbar_wait_warp(&bars->s_full[buf], use, abort);
+    bool ok = ptx::mbar_wait_warp_soon(&bars->s_full[buf], use, abort);
     if (!ok) mx_timeout(status, bars);
     // the four warps of a group meet at barriers below: they go on or give up together
     if constexpr (C::kStaged) ok = ptx::named_all(1 + grp, 128, ok);
@@ -475,16 +475,14 @@ __global__ void __launch_bounds__(MxEpi<NT>::kThreads, MxCfg<NT, KB>::kCtas)
   const uint32_t tmem = bars->tmem;
 
   if (warp == 0) {
-    if (lane == 0) {
-      ptx::prefetch_tmap(&tmx);
-      ptx::prefetch_tmap(&tmq);
+    {
       uint32_t it = 0, s = 0, ph = 1;               // ph: parity of the release to wait for
       bool ok = true;
-      for (MxWalk<true> w(vtiles, qtiles); ok && w.more() && !*abort; w.next()) {
+      for (MxWalk<true> w(vtiles, qtiles); ok && w.more(); w.next()) {
         const uint8_t* xsf = xs + w.v() * nkc * 512;
         const uint8_t* qsf = qs + w.q() * nkc * 512;
         for (int k = 0; k < nst; ++k) {
-          if (it >= C::kStages && !ptx::mbar_wait(&bars->empty[s], ph, abort)) {
+          if (it >= C::kStages && !ptx::mbar_wait_all(&bars->empty[s], ph, abort)) {
             mx_timeout(status, bars);
             ok = false;
             break;
@@ -493,33 +491,36 @@ __global__ void __launch_bounds__(MxEpi<NT>::kThreads, MxCfg<NT, KB>::kCtas)
           unsigned char* b = a + kMxBM * KB;
           unsigned char* sf = b + NT * KB;
           const uint32_t sfb = min(nkc - C::kAtoms * k, C::kAtoms) * 512;
-          ptx::mbar_arrive_expect_tx(&bars->full[s], kMxBM * KB + NT * KB + 2 * sfb);
-          ptx::tma_load_2d(a, &tmx, &bars->full[s], k * KB, (int)(w.v() * kMxBM));
-          ptx::bulk_load(sf, xsf + k * C::kSfB, sfb, &bars->full[s]);
-          ptx::tma_load_2d(b, &tmq, &bars->full[s], k * KB, (int)(w.q() * NT));
-          ptx::bulk_load(sf + C::kSfB, qsf + k * C::kSfB, sfb, &bars->full[s]);
+          if (ptx::elect_one()) {
+            ptx::mbar_arrive_expect_tx(&bars->full[s], kMxBM * KB + NT * KB + 2 * sfb);
+            ptx::tma_load_2d(a, &tmx, &bars->full[s], k * KB, (int)(w.v() * kMxBM));
+            ptx::bulk_load(sf, xsf + k * C::kSfB, sfb, &bars->full[s]);
+            ptx::tma_load_2d(b, &tmq, &bars->full[s], k * KB, (int)(w.q() * NT));
+            ptx::bulk_load(sf + C::kSfB, qsf + k * C::kSfB, sfb, &bars->full[s]);
+          }
+          __syncwarp();
           ++it;
           if (++s == C::kStages) s = 0, ph ^= 1;
         }
       }
-      if (*abort)  // let every copy this thread started land before the CTA exits
+      if (!ok || *abort)  // let every copy this warp started land before the CTA exits
         for (uint32_t k = (it > C::kStages ? it - C::kStages : 0); k < it; ++k)
           ptx::mbar_drain(&bars->full[k % C::kStages], (k / C::kStages) & 1);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    {
       constexpr uint64_t kHiK = KB == 128 ? ptx::sw128_hi(16, 1024) : ptx::sw64_hi(16, 512);
       uint32_t s = 0, ph = 0, it = 0, j = 0;
       bool ok = true;
-      for (MxWalk<true> w(vtiles, qtiles); ok && w.more() && !*abort; w.next(), ++j) {
+      for (MxWalk<true> w(vtiles, qtiles); ok && w.more(); w.next(), ++j) {
         const uint32_t buf = j & 1;
-        if (j >= 2 && !ptx::mbar_wait(&bars->s_empty[buf], ((j >> 1) - 1) & 1, abort)) {
+        if (j >= 2 && !ptx::mbar_wait_all(&bars->s_empty[buf], ((j >> 1) - 1) & 1, abort)) {
           ok = false;
           break;
         }
         const uint32_t d_tmem = tmem + buf * NT;
         for (int k = 0; k < nst; ++k, ++it) {
-          if (!ptx::mbar_wait(&bars->full[s], ph, abort)) {
+          if (!ptx::mbar_wait_all(&bars->full[s], ph, abort)) {
             ok = false;
             break;
           }
@@ -527,26 +528,30 @@ __global__ void __launch_bounds__(MxEpi<NT>::kThreads, MxCfg<NT, KB>::kCtas)
           const uint32_t b = a + kMxBM * KB, sf = b + NT * KB;
           const uint32_t sft = tmem + C::kSfCol + (it & 1) * 16;
           const int steps = min(2 * C::kAtoms, (nb + 1) / 2 - 2 * C::kAtoms * k);
+          const uint64_t da = ptx::sw128_desc(a, kHiK), db = ptx::sw128_desc(b, kHiK);
+          if (ptx::elect_one()) {
 #pragma unroll
           for (int h = 0; h < C::kAtoms; ++h)
             if (2 * h < steps) {
               ptx::tmem_cp_32x128(sft + 4 * h, ptx::rows16_desc(sf + 512 * h));
               ptx::tmem_cp_32x128(sft + 8 + 4 * h, ptx::rows16_desc(sf + C::kSfB + 512 * h));
             }
-          const uint64_t da = ptx::sw128_desc(a, kHiK), db = ptx::sw128_desc(b, kHiK);
 #pragma unroll
           for (int q = 0; q < 2 * C::kAtoms; ++q)
             if (q < steps)
               ptx::mma_mxf4_ss(d_tmem, da + 2 * q, db + 2 * q, ptx::idesc_mxf4(kMxBM, NT, 2 * (q & 1)),
                                sft + 4 * (q >> 1), sft + 8 + 4 * (q >> 1), k > 0 || q > 0);
           ptx::mma_commit(&bars->empty[s]);
+          }
+          __syncwarp();
           if (++s == C::kStages) s = 0, ph ^= 1;
         }
-        if (ok) ptx::mma_commit(&bars->s_full[buf]);
+        if (ok && ptx::elect_one()) ptx::mma_commit(&bars->s_full[buf]);
+        __syncwarp();
       }
-      if (!ok) mx_timeout(status, bars);
-      if (*abort) {  // wait for the products already issued before TMEM is freed
-        ptx::mma_commit(&bars->drain);
+      if (!ok) {  // wait for the products already issued before TMEM is freed
+        mx_timeout(status, bars);
+        if (ptx::elect_one()) ptx::mma_commit(&bars->drain);
         ptx::mbar_drain(&bars->drain, 0);
       }
     }
@@ -614,23 +619,25 @@ __global__ void __launch_bounds__(MxPackCfg<NT, KB>::kThreads, MxPackCfg<NT, KB>
   const uint32_t tmem = bars->tmem;
 
   if (warp == 0) {
-    if (lane == 0) {
-      ptx::prefetch_tmap(&tmq);
+    {
       uint32_t it = 0, s = 0, ph = 1, jq = 0;       // ph: parity of the release to wait for
       int64_t qt = -1;
       bool ok = true;
-      for (MxWalk<false> w(vtiles, qtiles); ok && w.more() && !*abort; w.next()) {
+      for (MxWalk<false> w(vtiles, qtiles); ok && w.more(); w.next()) {
         if (w.q() != qt) {                          // the next tile of queries
           qt = w.q();
           const uint32_t b = jq & 1;
-          if (jq >= 2 && !ptx::mbar_wait(&bars->q_empty[b], ((jq >> 1) - 1) & 1, abort)) ok = false;
+          if (jq >= 2 && !ptx::mbar_wait_all(&bars->q_empty[b], ((jq >> 1) - 1) & 1, abort)) ok = false;
           if (!ok) break;
-          ptx::mbar_arrive_expect_tx(&bars->q_full[b], NT * KB + nkc * 512);
-          ptx::tma_load_2d(qbuf + b * C::kQ, &tmq, &bars->q_full[b], 0, (int)(qt * NT));
-          ptx::bulk_load(qbuf + b * C::kQ + NT * KB, qs + qt * nkc * 512, nkc * 512, &bars->q_full[b]);
+          if (ptx::elect_one()) {
+            ptx::mbar_arrive_expect_tx(&bars->q_full[b], NT * KB + nkc * 512);
+            ptx::tma_load_2d(qbuf + b * C::kQ, &tmq, &bars->q_full[b], 0, (int)(qt * NT));
+            ptx::bulk_load(qbuf + b * C::kQ + NT * KB, qs + qt * nkc * 512, nkc * 512, &bars->q_full[b]);
+          }
+          __syncwarp();
           ++jq;
         }
-        if (it >= C::kRaw && !ptx::mbar_wait(&bars->empty[s], ph, abort)) {
+        if (it >= C::kRaw && !ptx::mbar_wait_all(&bars->empty[s], ph, abort)) {
           ok = false;
           break;
         }
@@ -638,14 +645,17 @@ __global__ void __launch_bounds__(MxPackCfg<NT, KB>::kThreads, MxPackCfg<NT, KB>
         const int rows = (int)min((int64_t)C::kSub * kMxBM, n - v0);
         const uint32_t bytes = (uint32_t)rows * nb * 16, sfb = (rows + 127) / 128 * nkc * 512;
         unsigned char* to = raw + s * C::kTile;
-        ptx::mbar_arrive_expect_tx(&bars->full[s], bytes + sfb);
-        ptx::bulk_load(to, xc + v0 * nb * 16, bytes, &bars->full[s]);
-        ptx::bulk_load(to + C::kSub * kMxBM * KB, xs + v0 / kMxBM * nkc * 512, sfb, &bars->full[s]);
+        if (ptx::elect_one()) {
+          ptx::mbar_arrive_expect_tx(&bars->full[s], bytes + sfb);
+          ptx::bulk_load(to, xc + v0 * nb * 16, bytes, &bars->full[s]);
+          ptx::bulk_load(to + C::kSub * kMxBM * KB, xs + v0 / kMxBM * nkc * 512, sfb, &bars->full[s]);
+        }
+        __syncwarp();
         ++it;
         if (++s == C::kRaw) s = 0, ph ^= 1;
       }
       if (!ok) mx_timeout(status, bars);
-      if (*abort) {  // let every copy this thread started land before the CTA exits
+      if (!ok || *abort) {  // let every copy this warp started land before the CTA exits
         for (uint32_t k = (it > C::kRaw ? it - C::kRaw : 0); k < it; ++k)
           ptx::mbar_drain(&bars->full[k % C::kRaw], (k / C::kRaw) & 1);
         for (uint32_t k = (jq > 2 ? jq - 2 : 0); k < jq; ++k)
@@ -653,30 +663,34 @@ __global__ void __launch_bounds__(MxPackCfg<NT, KB>::kThreads, MxPackCfg<NT, KB>
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    {
       constexpr uint64_t kHiK = KB == 128 ? ptx::sw128_hi(16, 1024) : ptx::sw64_hi(16, 512);
       const int steps = (nb + 1) / 2;
       uint32_t j = 0, jq = 0, buf = C::kBufs - 1, use = 1;   // buffer and parity of its phase
       int64_t qt = -1;
       bool ok = true;
-      for (MxWalk<false> w(vtiles, qtiles); ok && w.more() && !*abort; ++j) {
+      for (MxWalk<false> w(vtiles, qtiles); ok && w.more(); ++j) {
         if (++buf == C::kBufs) buf = 0, use ^= 1;
         // (the scale columns of the buffer's last step are free with its sums)
-        if (j >= C::kBufs && !ptx::mbar_wait(&bars->s_empty[buf], use ^ 1, abort)) ok = false;
+        if (j >= C::kBufs && !ptx::mbar_wait_all(&bars->s_empty[buf], use ^ 1, abort)) ok = false;
         if (!ok) break;
         if (w.q() != qt) {
           qt = w.q();
-          ok = ptx::mbar_wait(&bars->q_full[jq & 1], (jq >> 1) & 1, abort);
+          ok = ptx::mbar_wait_all(&bars->q_full[jq & 1], (jq >> 1) & 1, abort);
           if (!ok) break;
           const uint32_t sf = ptx::smem_u32(qbuf + (jq & 1) * C::kQ + NT * KB);
-          for (int h = 0; h < nkc; ++h)
-            ptx::tmem_cp_32x128(tmem + C::kSfQ + (jq & 1) * 4 * C::kAtoms + 4 * h, ptx::rows16_desc(sf + 512 * h));
+          if (ptx::elect_one())
+            for (int h = 0; h < nkc; ++h)
+              ptx::tmem_cp_32x128(tmem + C::kSfQ + (jq & 1) * 4 * C::kAtoms + 4 * h,
+                                  ptx::rows16_desc(sf + 512 * h));
+          __syncwarp();
           ++jq;
         }
         const uint32_t sfq = tmem + C::kSfQ + ((jq - 1) & 1) * 4 * C::kAtoms;
-        ok = ptx::mbar_wait(&bars->swz_full[buf], use, abort);
+        ok = ptx::mbar_wait_all(&bars->swz_full[buf], use, abort);
         if (!ok) break;
         const uint64_t db = ptx::sw128_desc(ptx::smem_u32(qbuf + ((jq - 1) & 1) * C::kQ), kHiK);
+        if (ptx::elect_one()) {
 #pragma unroll
         for (int u = 0; u < C::kSub; ++u) {
           const uint32_t a = ptx::smem_u32(swz + buf * C::kTile + u * C::kOne), sf = a + kMxBM * KB;
@@ -693,12 +707,15 @@ __global__ void __launch_bounds__(MxPackCfg<NT, KB>::kThreads, MxPackCfg<NT, KB>
         }
         ptx::mma_commit(&bars->swz_empty[buf]);
         ptx::mma_commit(&bars->s_full[buf]);
+        }
+        __syncwarp();
         w.next();
-        if (w.more() && w.q() != qt) ptx::mma_commit(&bars->q_empty[(jq - 1) & 1]);
+        if (w.more() && w.q() != qt && ptx::elect_one()) ptx::mma_commit(&bars->q_empty[(jq - 1) & 1]);
+        __syncwarp();
       }
-      if (!ok) mx_timeout(status, bars);
-      if (*abort) {  // wait for the products already issued before TMEM is freed
-        ptx::mma_commit(&bars->drain);
+      if (!ok) {  // wait for the products already issued before TMEM is freed
+        mx_timeout(status, bars);
+        if (ptx::elect_one()) ptx::mma_commit(&bars->drain);
         ptx::mbar_drain(&bars->drain, 0);
       }
     }
@@ -711,8 +728,8 @@ __global__ void __launch_bounds__(MxPackCfg<NT, KB>::kThreads, MxPackCfg<NT, KB>
     uint32_t s = 0, ph = 0, j = 0, buf = C::kBufs - 1, use = 1;
     for (MxWalk<false> w(vtiles, qtiles); w.more(); w.next(), ++j) {
       if (++buf == C::kBufs) buf = 0, use ^= 1;
-      bool ok = ptx::mbar_wait_warp(&bars->full[s], ph, abort);
-      if (ok && j >= C::kBufs) ok = ptx::mbar_wait_warp(&bars->swz_empty[buf], use ^ 1, abort);
+      bool ok = ptx::mbar_wait_warp_soon(&bars->full[s], ph, abort);
+      if (ok && j >= C::kBufs) ok = ptx::mbar_wait_warp_soon(&bars->swz_empty[buf], use ^ 1, abort);
       if (!ok) {
         mx_timeout(status, bars);
         break;
@@ -832,16 +849,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxPairCfg<T>::kThrea
   const int64_t p0 = blockIdx.x >> 1, np = gridDim.x >> 1, ntiles = vpairs * qtiles;
 
   if (warp == 0) {
-    if (lane == 0) {
-      ptx::prefetch_tmap(&tmx);
-      ptx::prefetch_tmap(&tmq);
+    {
       uint32_t it = 0, s = 0, ph = 1;
       bool ok = true;
-      for (int64_t t = p0; ok && t < ntiles && !*abort; t += np) {
+      for (int64_t t = p0; ok && t < ntiles; t += np) {
         const int64_t vp = t / qtiles, qt = t - vp * qtiles;
         const int64_t vt = 2 * vp + rank;           // (may be behind the last tile: zeros then)
         for (int k = 0; k < nst; ++k) {
-          if (it >= C::kStages && !ptx::mbar_wait(&bars->empty[s], ph, abort)) {
+          if (it >= C::kStages && !ptx::mbar_wait_all(&bars->empty[s], ph, abort)) {
             timeout();
             ok = false;
             break;
@@ -851,18 +866,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxPairCfg<T>::kThrea
           const uint32_t sfb = min(nkc - 2 * k, 2) * 512;
           const bool second = 2 * qt + 1 < qsf_tiles;
           const int64_t vsf = vt < vtiles ? vt : vtiles - 1;   // scales of what is not there: any
-          ptx::mbar_arrive_expect_tx(&bars->full[s], C::kA + C::kB + (second ? 3 : 2) * sfb);
-          ptx::tma_load_2d(a, &tmx, &bars->full[s], k * C::KB, (int)(vt * kMxBM));
-          ptx::tma_load_2d(a + C::kA, &tmq, &bars->full[s], k * C::KB, (int)(qt * C::NT + rank * (C::NT / 2)));
-          ptx::bulk_load(sf, xs + (vsf * nkc + 2 * k) * 512, sfb, &bars->full[s]);
-          ptx::bulk_load(sf + C::kSf, qs + (2 * qt * nkc + 2 * k) * 512, sfb, &bars->full[s]);
-          if (second)
-            ptx::bulk_load(sf + 2 * C::kSf, qs + ((2 * qt + 1) * nkc + 2 * k) * 512, sfb, &bars->full[s]);
+          if (ptx::elect_one()) {
+            ptx::mbar_arrive_expect_tx(&bars->full[s], C::kA + C::kB + (second ? 3 : 2) * sfb);
+            ptx::tma_load_2d(a, &tmx, &bars->full[s], k * C::KB, (int)(vt * kMxBM));
+            ptx::tma_load_2d(a + C::kA, &tmq, &bars->full[s], k * C::KB, (int)(qt * C::NT + rank * (C::NT / 2)));
+            ptx::bulk_load(sf, xs + (vsf * nkc + 2 * k) * 512, sfb, &bars->full[s]);
+            ptx::bulk_load(sf + C::kSf, qs + (2 * qt * nkc + 2 * k) * 512, sfb, &bars->full[s]);
+            if (second)
+              ptx::bulk_load(sf + 2 * C::kSf, qs + ((2 * qt + 1) * nkc + 2 * k) * 512, sfb, &bars->full[s]);
+          }
+          __syncwarp();
           ++it;
           if (++s == C::kStages) s = 0, ph ^= 1;
         }
       }
-      if (*abort)  // let every copy this thread started land before the CTA exits
+      if (!ok || *abort)  // let every copy this warp started land before the CTA exits
         for (uint32_t k = (it > C::kStages ? it - C::kStages : 0); k < it; ++k)
           ptx::mbar_drain(&bars->full[k % C::kStages], (k / C::kStages) & 1);
     }
@@ -872,7 +890,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxPairCfg<T>::kThrea
       bool ok = true;
       for (int64_t t = p0; ok && t < ntiles && !*abort; t += np)
         for (int k = 0; k < nst; ++k) {
-          if (!ptx::mbar_wait(&bars->full[s], ph, abort)) {
+          if (!ptx::mbar_wait_soon(&bars->full[s], ph, abort)) {
             timeout();
             ok = false;
             break;
@@ -882,27 +900,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxPairCfg<T>::kThrea
         }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    {
       constexpr uint64_t kHiK = ptx::sw128_hi(16, 1024);
       uint32_t s = 0, ph = 0, j = 0, cp = 0;
       bool ok = true;
-      for (int64_t t = p0; ok && t < ntiles && !*abort; t += np, ++j) {
+      for (int64_t t = p0; ok && t < ntiles; t += np, ++j) {
         const uint32_t buf = j & 1;
-        if (j >= 2 && !ptx::mbar_wait_cluster(&bars->s_empty[buf], ((j >> 1) - 1) & 1, abort)) ok = false;
-        if (ok && j >= 1 && !ptx::mbar_wait_cluster(&bars->overlap, (j - 1) & 1, abort)) ok = false;
+        if (j >= 2) ok = ptx::mbar_wait_cluster_all(&bars->s_empty[buf], ((j >> 1) - 1) & 1, abort);
+        if (ok && j >= 1) ok = ptx::mbar_wait_cluster_all(&bars->overlap, (j - 1) & 1, abort);
         if (!ok) break;
         const uint32_t d_tmem = tmem + (buf ? C::kAcc1 : 0);
         for (int k = 0; k < nst; ++k) {
-          ok = ptx::mbar_wait(&bars->full[s], ph, abort) && ptx::mbar_wait_cluster(&bars->peer[s], ph, abort);
+          ok = ptx::mbar_wait_all(&bars->full[s], ph, abort);
+          if (ok) ok = ptx::mbar_wait_cluster_all(&bars->peer[s], ph, abort);
           if (!ok) break;
           const uint32_t a = ptx::smem_u32(ring + s * C::kStage), sf = a + C::kA + C::kB;
           const uint64_t da = ptx::sw128_desc(a, kHiK), db = ptx::sw128_desc(a + C::kA, kHiK);
           const int steps = min(4, (nb + 1) / 2 - 4 * k);
+          if (ptx::elect_one()) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             if (2 * h < steps) {
               // 12 columns of scales for 128 dimensions: the vectors' 4, the queries' 8
-              const uint32_t sft = tmem + C::kSfCol + (cp++ & 1) * 12;
+              const uint32_t sft = tmem + C::kSfCol + ((cp + h) & 1) * 12;
               ptx::tmem_cp_32x128_pair(sft, ptx::rows16_desc(sf + 512 * h));
               ptx::tmem_cp_32x128_pair(sft + 4, ptx::rows16_desc(sf + C::kSf + 512 * h));
               ptx::tmem_cp_32x128_pair(sft + 8, ptx::rows16_desc(sf + 2 * C::kSf + 512 * h));
@@ -913,13 +933,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxPairCfg<T>::kThrea
                                      sft, sft + 4, k > 0 || q > 0);
             }
           ptx::mma_commit_pair(&bars->empty[s]);
+          }
+          __syncwarp();
+          cp += (steps + 1) / 2;
           if (++s == C::kStages) s = 0, ph ^= 1;
         }
-        if (ok) ptx::mma_commit_pair(&bars->s_full[buf]);
+        if (ok && ptx::elect_one()) ptx::mma_commit_pair(&bars->s_full[buf]);
+        __syncwarp();
       }
-      if (!ok) timeout();
-      if (*abort) {  // wait for the products already issued before TMEM is freed
-        ptx::mma_commit_pair(&bars->drain);
+      if (!ok) {  // wait for the products already issued before TMEM is freed
+        timeout();
+        if (ptx::elect_one()) ptx::mma_commit_pair(&bars->drain);
         ptx::mbar_drain(&bars->drain, 0);
       }
     }
@@ -932,7 +956,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxPairCfg<T>::kThrea
       const uint32_t buf = j & 1;
       const int64_t n0 = (2 * vp + rank) * kMxBM, row = n0 + q * 32 + lane;
       const float bv = bias && row < n ? __ldg(bias + row) : 0.f;
-      bool ok = ptx::mbar_wait_warp(&bars->s_full[buf], (j >> 1) & 1, abort);
+      bool ok = ptx::mbar_wait_warp_soon(&bars->s_full[buf], (j >> 1) & 1, abort);
       if (!ok) timeout();
       ok = ptx::named_all(1 + grp, 128, ok);        // the four warps of a group go on or give up together
       if (!ok) break;
