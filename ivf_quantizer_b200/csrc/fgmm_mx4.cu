@@ -772,8 +772,9 @@ __global__ void __launch_bounds__(MxPackCfg<NT, KB>::kThreads, MxPackCfg<NT, KB>
 // Many queries of long vectors: the products decide, and what bounds them is how fast operands come
 // into shared memory (TMA moves about 30 bytes a clock and SM).  A pair of CTAs shares a tile of 256
 // vectors x 256 queries: each loads its 128 vectors and half of the queries, 32 KB for 128 x 256 x 256
-// products, half of what a tile of 128 x 128 needs.  The first CTA's thread issues the products of both;
-// a thread of the second passes on that its stage is full.
+// products, half of what a tile of 128 x 128 needs.  The first CTA issues the products of both, and the
+// copies of both are counted on its barriers (a thread of the second passing on that its stage is full
+// cost a third of the time).
 //
 // Two accumulators of 256 columns and the scales do not fit into 512 columns, so the accumulators
 // overlap by 32: the epilogue drains those first, and the next tile's products wait for them alone.
@@ -793,7 +794,7 @@ struct MxPairCfg {
 };
 
 struct MxPairBars {
-  uint64_t full[kMxMaxStages], peer[kMxMaxStages], empty[kMxMaxStages];
+  uint64_t full[kMxMaxStages], empty[kMxMaxStages];
   uint64_t s_full[2], s_empty[2], overlap, drain;
   uint32_t tmem;
   int abort;
@@ -803,8 +804,8 @@ static_assert(sizeof(MxPairBars) <= 512, "barriers");
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxPairCfg<T>::kThreads, 1)
     mx4_scores_pair_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmq,
-                           const uint8_t* __restrict__ xs, const uint8_t* __restrict__ qs, int64_t n,
-                           int64_t m, int nb, int64_t vpairs, int64_t qtiles, float alpha,
+                           const __grid_constant__ CUtensorMap tmxs, const __grid_constant__ CUtensorMap tmqs,
+                           int64_t n, int64_t m, int nb, int64_t vpairs, int64_t qtiles, float alpha,
                            const float* __restrict__ bias, T* __restrict__ out, int64_t ldo, int* status) {
   using C = MxPairCfg<T>;
   extern __shared__ unsigned char smem_raw[];
@@ -816,11 +817,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxPairCfg<T>::kThrea
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = blockIdx.x & 1;
   const int nkc = (nb + 3) / 4, nst = (nkc + 1) / 2;
-  const int64_t vtiles = (n + kMxBM - 1) / kMxBM, qsf_tiles = (m + kMxBM - 1) / kMxBM;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       ptx::mbar_init(&bars->full[s], 1);
-      ptx::mbar_init(&bars->peer[s], 1);
       ptx::mbar_init(&bars->empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -854,8 +853,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxPairCfg<T>::kThrea
       bool ok = true;
       for (int64_t t = p0; ok && t < ntiles; t += np) {
         const int64_t vp = t / qtiles, qt = t - vp * qtiles;
-        const int64_t vt = 2 * vp + rank;           // (may be behind the last tile: zeros then)
-        for (int k = 0; k < nst; ++k) {
+        const int vt = (int)(2 * vp + rank), qh = (int)(qt * C::NT + rank * (C::NT / 2));
+        for (int k = 0; k < nst; ++k) {             // (what is behind the last row or block reads as 0)
           if (it >= C::kStages && !ptx::mbar_wait_all(&bars->empty[s], ph, abort)) {
             timeout();
             ok = false;
@@ -863,44 +862,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxPairCfg<T>::kThrea
           }
           unsigned char* a = ring + s * C::kStage;
           unsigned char* sf = a + C::kA + C::kB;
-          const uint32_t sfb = min(nkc - 2 * k, 2) * 512;
-          const bool second = 2 * qt + 1 < qsf_tiles;
-          const int64_t vsf = vt < vtiles ? vt : vtiles - 1;   // scales of what is not there: any
+          const uint32_t bar = ptx::cluster_addr(&bars->full[s], 0);
           if (ptx::elect_one()) {
-            ptx::mbar_arrive_expect_tx(&bars->full[s], C::kA + C::kB + (second ? 3 : 2) * sfb);
-            ptx::tma_load_2d(a, &tmx, &bars->full[s], k * C::KB, (int)(vt * kMxBM));
-            ptx::tma_load_2d(a + C::kA, &tmq, &bars->full[s], k * C::KB, (int)(qt * C::NT + rank * (C::NT / 2)));
-            ptx::bulk_load(sf, xs + (vsf * nkc + 2 * k) * 512, sfb, &bars->full[s]);
-            ptx::bulk_load(sf + C::kSf, qs + (2 * qt * nkc + 2 * k) * 512, sfb, &bars->full[s]);
-            if (second)
-              ptx::bulk_load(sf + 2 * C::kSf, qs + ((2 * qt + 1) * nkc + 2 * k) * 512, sfb, &bars->full[s]);
+            if (rank == 0) ptx::mbar_arrive_expect_tx(&bars->full[s], 2 * C::kStage);
+            ptx::tma_load_2d_pair(a, &tmx, bar, k * C::KB, vt * kMxBM);
+            ptx::tma_load_2d_pair(a + C::kA, &tmq, bar, k * C::KB, qh);
+            ptx::tma_load_3d_pair(sf, &tmxs, bar, 0, 2 * k, vt);
+            ptx::tma_load_3d_pair(sf + C::kSf, &tmqs, bar, 0, 2 * k, (int)(2 * qt));
           }
           __syncwarp();
           ++it;
           if (++s == C::kStages) s = 0, ph ^= 1;
         }
       }
-      if (!ok || *abort)  // let every copy this warp started land before the CTA exits
-        for (uint32_t k = (it > C::kStages ? it - C::kStages : 0); k < it; ++k)
-          ptx::mbar_drain(&bars->full[k % C::kStages], (k / C::kStages) & 1);
-    }
-  } else if (warp == 1 && rank == 1) {
-    if (lane == 0) {
-      uint32_t s = 0, ph = 0;
-      bool ok = true;
-      for (int64_t t = p0; ok && t < ntiles && !*abort; t += np)
-        for (int k = 0; k < nst; ++k) {
-          if (!ptx::mbar_wait_soon(&bars->full[s], ph, abort)) {
-            timeout();
-            ok = false;
-            break;
-          }
-          ptx::mbar_arrive_cluster(&bars->peer[s], 0);
-          if (++s == C::kStages) s = 0, ph ^= 1;
-        }
+      if (!ok || *abort) {  // let every copy this warp started land before the CTA exits
+        if (rank == 0)
+          for (uint32_t k = (it > C::kStages ? it - C::kStages : 0); k < it; ++k)
+            ptx::mbar_drain(&bars->full[k % C::kStages], (k / C::kStages) & 1);
+        else                                        // (its copies are counted over there: 1 ms is ample)
+          for (const uint64_t t0 = ptx::globaltimer_ns(); ptx::globaltimer_ns() - t0 < 1000000;) {}
+      }
     }
   } else if (warp == 1) {
-    {
+    if (rank == 0) {
       constexpr uint64_t kHiK = ptx::sw128_hi(16, 1024);
       uint32_t s = 0, ph = 0, j = 0, cp = 0;
       bool ok = true;
@@ -911,8 +895,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxPairCfg<T>::kThrea
         if (!ok) break;
         const uint32_t d_tmem = tmem + (buf ? C::kAcc1 : 0);
         for (int k = 0; k < nst; ++k) {
-          ok = ptx::mbar_wait_all(&bars->full[s], ph, abort);
-          if (ok) ok = ptx::mbar_wait_cluster_all(&bars->peer[s], ph, abort);
+          ok = ptx::mbar_wait_cluster_all(&bars->full[s], ph, abort);
           if (!ok) break;
           const uint32_t a = ptx::smem_u32(ring + s * C::kStage), sf = a + C::kA + C::kB;
           const uint64_t da = ptx::sw128_desc(a, kHiK), db = ptx::sw128_desc(a + C::kA, kHiK);
@@ -1038,6 +1021,19 @@ bool mx_tmap(CUtensorMap* map, const uint8_t* codes, int nb, int64_t rows, int b
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Scale tiles [rows of tiles][tiles of a row][512 bytes] as boxes of 2 of a row x `box_rows`.
+bool mx_tmap_scales(CUtensorMap* map, const uint8_t* scales, int nb, int64_t rows, int box_rows) {
+  EncodeTiledFn enc = mx_encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t nkc = (cuuint64_t)(nb + 3) / 4;
+  const cuuint64_t dims[3] = {128, nkc, (cuuint64_t)(rows + 127) / 128};
+  const cuuint64_t strides[2] = {512, 512 * nkc};
+  const cuuint32_t box[3] = {128, 2, (cuuint32_t)box_rows}, one[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t*>(scales), dims, strides, box,
+             one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct MxArgs {
   const uint8_t *qc, *qs, *xc, *xs;
   int64_t m, n;
@@ -1099,8 +1095,9 @@ cudaError_t mx_scores(const MxArgs& a) {
 template <typename T>
 cudaError_t mx_scores_pair(const MxArgs& a) {
   using C = MxPairCfg<T>;
-  CUtensorMap tmx, tmq;
-  if (!mx_tmap(&tmx, a.xc, a.nb, a.n, C::KB, kMxBM) || !mx_tmap(&tmq, a.qc, a.nb, a.m, C::KB, C::NT / 2))
+  CUtensorMap tmx, tmq, tmxs, tmqs;
+  if (!mx_tmap(&tmx, a.xc, a.nb, a.n, C::KB, kMxBM) || !mx_tmap(&tmq, a.qc, a.nb, a.m, C::KB, C::NT / 2) ||
+      !mx_tmap_scales(&tmxs, a.xs, a.nb, a.n, 1) || !mx_tmap_scales(&tmqs, a.qs, a.nb, a.m, 2))
     return cudaErrorInvalidValue;
   auto* k = mx4_scores_pair_kernel<T>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
@@ -1110,7 +1107,7 @@ cudaError_t mx_scores_pair(const MxArgs& a) {
   if (e != cudaSuccess) return e;
   const int64_t vp = (a.n + 2 * kMxBM - 1) / (2 * kMxBM), qt = (a.m + C::NT - 1) / C::NT;
   const int64_t pairs = vp * qt < sms / 2 ? vp * qt : sms / 2;
-  k<<<(unsigned)(2 * pairs), C::kThreads, C::kSmem, a.s>>>(tmx, tmq, a.xs, a.qs, a.n, a.m, a.nb, vp, qt, a.alpha,
+  k<<<(unsigned)(2 * pairs), C::kThreads, C::kSmem, a.s>>>(tmx, tmq, tmxs, tmqs, a.n, a.m, a.nb, vp, qt, a.alpha,
                                                            a.bias, static_cast<T*>(a.out), a.ldo, a.status);
   return cudaGetLastError();
 }
