@@ -947,35 +947,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxPairCfg<T>::kThrea
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (buf ? C::kAcc1 : 0) + grp * 64;
       const int len = (int)max((int64_t)0, min((int64_t)kMxBM, n - n0));
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        const int c = 16 * (buf ? i : 3 - i);       // the shared columns first
-        uint32_t u[16];
-        ptx::tmem_ld16(acc + c, u);
+      for (int i = 0; i < 2; ++i) {                 // 32 columns at a time, the shared ones first
+        const int c = 32 * (buf ? i : 1 - i);
+        uint32_t u[32];
+        ptx::tmem_ld32(acc + c, u);
         ptx::tmem_wait_ld();
-        if (i == 1 && grp == (buf ? 0 : C::kGroups - 1)) {
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_cluster(&bars->overlap, 0);
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (i == 0 && grp == (buf ? 0 : C::kGroups - 1)) ptx::mbar_arrive_cluster(&bars->overlap, 0);
+          if (i == 1) ptx::mbar_arrive_cluster(&bars->s_empty[buf], 0);
         }
-        if (i == 3) {
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_cluster(&bars->s_empty[buf], 0);
-        }
-        const int64_t mc = qt * C::NT + grp * 64 + c;
-        const int rows = (int)min((int64_t)16, m - mc);
-        unsigned char* st = outbuf + (grp * 2 + (i & 1)) * 16 * C::kOutRow;
-        const int pm = (int)(((uintptr_t)out / sizeof(T) + (uintptr_t)mc * ldo + n0) % VN), dp = (int)(ldo % VN);
-        ptx::bulk_wait_read<1>();
-        ptx::named_sync(1 + grp, 128);
-        T* mine = reinterpret_cast<T*>(st) + q * 32 + lane;
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          mx_cvt(fmaf(alpha, __uint_as_float(u[e]), bv),
-                 mine[e * (C::kOutRow / sizeof(T)) + ((pm + e * dp) & (VN - 1))]);
-        ptx::fence_proxy_async_smem();
-        ptx::named_sync(1 + grp, 128);
-        mx_rows_out<T>(st, C::kOutRow, q, lane, rows, len, pm, dp, out + mc * ldo + n0, ldo);
+        for (int half = 0; half < 2; ++half) {
+          const int64_t mc = qt * C::NT + grp * 64 + c + 16 * half;
+          const int rows = (int)min((int64_t)16, m - mc);
+          unsigned char* st = outbuf + (grp * 2 + half) * 16 * C::kOutRow;
+          const int pm = (int)(((uintptr_t)out / sizeof(T) + (uintptr_t)mc * ldo + n0) % VN);
+          const int dp = (int)(ldo % VN);
+          ptx::bulk_wait_read<1>();
+          ptx::named_sync(1 + grp, 128);
+          T* mine = reinterpret_cast<T*>(st) + q * 32 + lane;
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            mx_cvt(fmaf(alpha, __uint_as_float(u[16 * half + e]), bv),
+                   mine[e * (C::kOutRow / sizeof(T)) + ((pm + e * dp) & (VN - 1))]);
+          ptx::fence_proxy_async_smem();
+          ptx::named_sync(1 + grp, 128);
+          mx_rows_out<T>(st, C::kOutRow, q, lane, rows, len, pm, dp, out + mc * ldo + n0, ldo);
+        }
       }
     }
     ptx::bulk_wait_read<0>();
