@@ -373,15 +373,24 @@ __device__ __forceinline__ void mx_epilogue(int warp, MxBars* bars, unsigned cha
   const int q = warp & 3, grp = warp >> 2, c0 = grp * kColsWarp;
   const uint32_t lane_base = (uint32_t)(q * 32) << 16;
   uint32_t buf = BUFS - 1, use = 1;                      // buffer and parity of its phase
+  MxWalk<QFAST> ahead(vtiles, qtiles);
+  float next_bias[SUB];
+  auto load_bias = [&] {
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) {
+      const int64_t row = (ahead.v() * SUB + u) * kMxBM + q * 32 + lane;
+      next_bias[u] = bias && ahead.more() && row < n ? __ldg(bias + row) : 0.f;
+    }
+  };
+  load_bias();
   for (MxWalk<QFAST> w(vtiles, qtiles); w.more(); w.next()) {
     const int64_t m0 = w.q() * NT + c0;
     if (++buf == BUFS) buf = 0, use ^= 1;
     float bvs[SUB];
 #pragma unroll
-    for (int u = 0; u < SUB; ++u) {
-      const int64_t row = (w.v() * SUB + u) * kMxBM + q * 32 + lane;
-      bvs[u] = bias && row < n ? __ldg(bias + row) : 0.f;
-    }
+    for (int u = 0; u < SUB; ++u) bvs[u] = next_bias[u];
+    ahead.next();                                     // the next step's, while this one is drained
+    load_bias();
     bool ok = ptx::mbar_wait_warp_soon(&bars->s_full[buf], use, abort);
     if (!ok) mx_timeout(status, bars);
     // the four warps of a group meet at barriers below: they go on or give up together
@@ -934,11 +943,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxPairCfg<T>::kThrea
     constexpr int VN = 16 / sizeof(T);
     const int q = warp & 3, grp = (warp - 4) >> 2;
     uint32_t j = 0;
+    auto bias_of = [&](int64_t t) {
+      const int64_t row = (2 * (t / qtiles) + rank) * kMxBM + q * 32 + lane;
+      return bias && t < ntiles && row < n ? __ldg(bias + row) : 0.f;
+    };
+    float next_bias = bias_of(p0);
     for (int64_t t = p0; t < ntiles; t += np, ++j) {
       const int64_t vp = t / qtiles, qt = t - vp * qtiles;
       const uint32_t buf = j & 1;
-      const int64_t n0 = (2 * vp + rank) * kMxBM, row = n0 + q * 32 + lane;
-      const float bv = bias && row < n ? __ldg(bias + row) : 0.f;
+      const int64_t n0 = (2 * vp + rank) * kMxBM;
+      const float bv = next_bias;
+      next_bias = bias_of(t + np);                  // the next tile's, while this one is drained
       bool ok = ptx::mbar_wait_warp_soon(&bars->s_full[buf], (j >> 1) & 1, abort);
       if (!ok) timeout();
       ok = ptx::named_all(1 + grp, 128, ok);        // the four warps of a group go on or give up together
