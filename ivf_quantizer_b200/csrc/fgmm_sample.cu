@@ -194,6 +194,19 @@ struct SmShared {
   int owner;
 };
 
+struct SmArgs {
+  const void* logits;
+  int V;
+  int64_t ld;
+  const float* temperature;
+  const int32_t* top_k;
+  const float *top_p, *min_p;
+  const double* u;
+  int32_t* ids;
+  float* prob;
+  int slice;                                // values a CTA takes
+};
+
 template <typename T, int THREADS, bool RES>
 struct Sampler {
   using S = SmShared<THREADS>;
@@ -247,10 +260,10 @@ struct Sampler {
   __device__ __forceinline__ uint32_t index(int v, int g) const {
     return (uint32_t)(first + v * V::N + 4 * g - phase);
   }
-  // f(four values, index of the first) for the groups of the slice that hold a value of at least
-  // `from`, each warp its own contiguous part.
-  template <typename F>
-  __device__ __forceinline__ void each(float from, F f) {
+  // f(four values, index of the first) for the groups of the slice that hold a value in [from, to]
+  // (WINDOW) or of at least `from`, each warp its own contiguous part.
+  template <bool WINDOW = false, typename F>
+  __device__ __forceinline__ void each(float from, F f, float to = 0.f) {
     constexpr int U = RES ? 1 : 4;          // loads in flight
     const int v1 = min(nvec, (warp + 1) * vpw);
     for (int v = warp * vpw + lane; v < v1; v += 32 * U) {
@@ -264,8 +277,15 @@ struct Sampler {
         for (int g = 0; g < V::N / 4; ++g) {
           float x[4];
           V::get(q[i], g, x);
-          if (fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= from && (i == 0 || v + 32 * i < v1))
-            f(x, index(v + 32 * i, g));
+          bool hit;
+          if constexpr (WINDOW) {
+            hit = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) hit |= x[e] >= from && x[e] <= to;
+          } else {
+            hit = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= from;
+          }
+          if (hit && (i == 0 || v + 32 * i < v1)) f(x, index(v + 32 * i, g));
         }
     }
   }
@@ -426,19 +446,42 @@ struct Sampler {
     }
   }
 
+  // The logits of a bin, a few roundings wider: which of them are in it is asked one by one.
+  __device__ __forceinline__ void window(int bin, float from, float& low, float& high) const {
+    const double unit = 1.0 / r.c, x0 = r.topd + (-bin - 0.5) * unit, x1 = x0 + unit;
+    const double slack = 1e-6 * (fabs(r.topd) + fabs(x0) + unit);
+    low = fmaxf(from, __double2float_rd(x0 - slack)), high = __double2float_ru(x1 + slack);
+  }
+
+  // Block-wide sum, every thread receives it.
+  __device__ __forceinline__ uint64_t sum_all(uint64_t w) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+    __syncthreads();
+    if (lane == 0) s.wsum[warp] = w;
+    __syncthreads();
+    w = s.wsum[lane % W];
+#pragma unroll
+    for (int o = 1; o < W; o <<= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+    return w;
+  }
+
+  // The whole rest of a row whose top-k border lies in bin `bin`, when so few tokens (n <= THREADS)
+  // lie in the bins down to it that a thread can take one: CTA 0 collects them, and every thread
+  // counts the others against its own, first by place (top-k, top-p), then by index (the draw).
+  __device__ void few(int bin, uint32_t n, int k, float p, uint64_t least, double u, float from,
+                      const SmArgs& a, int64_t rw, float t);
+
   // The place of the last token that a truncation keeps: the k-th (by_count), or that at which the
-  // running mass reaches need.  The cluster's histogram over bins is there; `from`: tokens below
-  // are not in it.
+  // running mass reaches need.  The border's bin has been picked from the cluster's histogram; `from`:
+  // tokens below are not in it.
   __device__ uint64_t find(bool by_count, uint32_t k, double need, float from, uint64_t limit) {
-    pick(by_count, k, need, 0ull, 0u);
     if (s.bin == kSmBins) return limit;     // all that weighs anything is kept
     const int bin0 = s.bin;
     uint64_t above = s.above_mass;
     uint32_t above_cnt = s.above_cnt;
-    // logits of the bin, a few roundings wider; which of them are in it is asked one by one
-    const double unit = 1.0 / r.c, x0 = r.topd + (-bin0 - 0.5) * unit, x1 = x0 + unit;
-    const double slack = 1e-6 * (fabs(r.topd) + fabs(x0) + unit);
-    const float low = fmaxf(from, __double2float_rd(x0 - slack)), high = __double2float_ru(x1 + slack);
+    float low, high;
+    window(bin0, from, low, high);
     uint64_t lo = 0, hi = kSmAll;
     for (int level = 0;; ++level) {
       auto member = [&](float x, uint32_t i, uint64_t& c) {
@@ -448,7 +491,7 @@ struct Sampler {
       };
       // collect them in CTA 0 (the counters are 0 since the exchange); if they are too many for its
       // list, split them first
-      each(low, [&](const float (&x)[4], uint32_t i) {
+      each<true>(low, [&](const float (&x)[4], uint32_t i) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           uint64_t c;
@@ -457,7 +500,7 @@ struct Sampler {
             if (j < (uint32_t)kList) *at(&s.list[j], 0) = c;
           }
         }
-      });
+      }, high);
       sync();
       const uint32_t n = *at(&s.nlist, 0);
       if (n <= (uint32_t)kList) {
@@ -467,13 +510,13 @@ struct Sampler {
       }
       if (level == 0) {                     // the range of places in the bin
         uint64_t a = kSmAll, b = 0;
-        each(low, [&](const float (&x)[4], uint32_t i) {
+        each<true>(low, [&](const float (&x)[4], uint32_t i) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint64_t c;
             if (x[e] >= low && member(x[e], i + e, c)) a = min(a, c), b = max(b, c);
           }
-        });
+        }, high);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
           a = min(a, (uint64_t)__shfl_xor_sync(0xffffffffu, a, o));
@@ -491,7 +534,7 @@ struct Sampler {
       }
       const int shift = max(0, 64 - __clzll((long long)(hi - lo)) - 10);   // at most 1024 parts
       clear();
-      each(low, [&](const float (&x)[4], uint32_t i) {
+      each<true>(low, [&](const float (&x)[4], uint32_t i) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           uint64_t c;
@@ -502,7 +545,7 @@ struct Sampler {
             else add(&s.h.lo[b], &s.h.hi[b], sm_weight(x[e], r, s.table, bin));
           }
         }
-      });
+      }, high);
       exchange(!by_count, by_count);
       pick(by_count, k, need, above, above_cnt);
       const int bin = s.bin;
@@ -514,18 +557,49 @@ struct Sampler {
   }
 };
 
-struct SmArgs {
-  const void* logits;
-  int V;
-  int64_t ld;
-  const float* temperature;
-  const int32_t* top_k;
-  const float *top_p, *min_p;
-  const double* u;
-  int32_t* ids;
-  float* prob;
-  int slice;                                // values a CTA takes
-};
+template <typename T, int THREADS, bool RES>
+__device__ void Sampler<T, THREADS, RES>::few(int bin, uint32_t n, int k, float p, uint64_t least, double u,
+                                              float from, const SmArgs& a, int64_t rw, float t) {
+  float low, high;
+  window(bin, from, low, high);
+  each(low, [&](const float (&x)[4], uint32_t i) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (x[e] >= low && (x[e] > high || sm_bin(x[e], r) <= bin)) {
+        const uint32_t j = atomicAdd(at(&s.nlist, 0), 1u);
+        if (j < (uint32_t)THREADS) *at(&s.list[j], 0) = sm_place(x[e], i + e);
+      }
+  });
+  sync();                                   // the last access to another CTA's memory is before this
+  if (rank != 0) return;
+  const uint32_t me = threadIdx.x;
+  const uint64_t mine = me < n ? s.list[me] : kSmAll;
+  const float x = sm_place_value(mine);
+  int b;
+  const uint64_t w = me < n ? sm_weight(x, r, s.table, b) : 0ull;
+  s.m0[me] = w;
+  __syncthreads();
+  uint32_t before = 0;
+  uint64_t mass = 0;
+#pragma unroll 4
+  for (uint32_t j = 0; j < n; ++j)
+    if (s.list[j] < mine) ++before, mass += s.m0[j];
+  const uint64_t wk = before < (uint32_t)k ? w : 0ull;
+  const uint64_t whole = sum_all(wk);       // (its barriers also end the reading of m0)
+  const bool kept = wk > 0 && wk >= least && (before == 0 || (double)mass < (double)p * (double)whole || p >= 1.f);
+  s.m0[me] = kept ? w : 0ull;
+  const uint64_t total = sum_all(kept ? w : 0ull);
+  const uint64_t target = min((uint64_t)(u * (double)total), total - 1);
+  if (!kept) return;
+  uint64_t run = 0;
+#pragma unroll 4
+  for (uint32_t j = 0; j < n; ++j)
+    if ((uint32_t)s.list[j] < (uint32_t)mine) run += s.m0[j];
+  if (run <= target && run + w > target) {
+    a.ids[rw] = (int32_t)(uint32_t)mine;
+    if (a.prob) a.prob[rw] = sm_prob(x, r, s.table, t, total);
+  }
+}
 
 template <typename T, int THREADS, bool RES>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const SmArgs a) {
@@ -623,6 +697,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
           if (x[e] >= from) atomicAdd(&s.h.cnt[sm_bin(x[e], r)], 1u);
       });
       z.exchange(false, true);
+      z.pick(true, (uint32_t)k, 0.0, 0ull, 0u);
+      const uint32_t n = s.above_cnt + s.bin_cnt;
+      if (s.bin < kSmBins && n <= (uint32_t)THREADS) {
+        z.few(s.bin, n, k, p, sm_min_weight(mp), un, from, a, rw, t);
+        return;
+      }
       border = z.find(true, (uint32_t)k, 0.0, from, border);
       if (border != kSmAll) from = fmaxf(from, sm_place_value(border));
     }
@@ -653,6 +733,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
       __syncthreads();
       for (int q = 0; q < Sm::W; ++q) whole += s.wsum[q];
       __syncthreads();
+      z.pick(false, 0u, (double)p * (double)whole, 0ull, 0u);
       border = z.find(false, 0u, (double)p * (double)whole, from, border);
       if (border != kSmAll) from = fmaxf(from, sm_place_value(border));
     }
@@ -669,9 +750,22 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
     } else {
       z.weights(x, w, bin);
     }
+    bool tie = false;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = (x[e] > from || (x[e] == from && i + e <= ib)) && w[e] >= least ? w[e] : 0ull;
+    for (int e = 0; e < 4; ++e) {
+      w[e] = x[e] >= from ? w[e] : 0ull;
+      tie |= x[e] == from;
+    }
+    if (tie) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (x[e] == from && i + e > ib) w[e] = 0ull;
+    }
+    if (least > 0) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (w[e] < least) w[e] = 0ull;
+    }
   };
   uint64_t mass = 0;
   z.each(from, [&](const float (&x)[4], uint32_t i) {
