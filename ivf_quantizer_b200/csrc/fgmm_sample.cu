@@ -466,11 +466,12 @@ struct Sampler {
     return w;
   }
 
-  // The whole rest of a row whose top-k border lies in bin `bin`, when so few tokens (n <= THREADS)
+  // The whole rest of a row whose border lies in bin `bin`, when so few tokens (n <= THREADS)
   // lie in the bins down to it that a thread can take one: CTA 0 collects them, and every thread
   // counts the others against its own, first by place (top-k, top-p), then by index (the draw).
-  __device__ void few(int bin, uint32_t n, int k, float p, uint64_t least, double u, float from,
-                      const SmArgs& a, int64_t rw, float t);
+  // `whole`: the mass that top-p refers to, 0 for that of the k tokens.
+  __device__ void few(int bin, uint32_t n, uint32_t k, uint64_t whole, float p, uint64_t least, double u,
+                      float from, const SmArgs& a, int64_t rw, float t);
 
   // The place of the last token that a truncation keeps: the k-th (by_count), or that at which the
   // running mass reaches need.  The border's bin has been picked from the cluster's histogram; `from`:
@@ -558,8 +559,9 @@ struct Sampler {
 };
 
 template <typename T, int THREADS, bool RES>
-__device__ void Sampler<T, THREADS, RES>::few(int bin, uint32_t n, int k, float p, uint64_t least, double u,
-                                              float from, const SmArgs& a, int64_t rw, float t) {
+__device__ void Sampler<T, THREADS, RES>::few(int bin, uint32_t n, uint32_t k, uint64_t whole, float p,
+                                              uint64_t least, double u, float from, const SmArgs& a,
+                                              int64_t rw, float t) {
   float low, high;
   window(bin, from, low, high);
   each(low, [&](const float (&x)[4], uint32_t i) {
@@ -572,30 +574,38 @@ __device__ void Sampler<T, THREADS, RES>::few(int bin, uint32_t n, int k, float 
   });
   sync();                                   // the last access to another CTA's memory is before this
   if (rank != 0) return;
-  const uint32_t me = threadIdx.x;
+  // G lanes a token, each comparing it with every G-th
+  int G = 1;
+  while (G < 32 && 2 * G * n <= (uint32_t)THREADS) G *= 2;
+  const uint32_t me = threadIdx.x / G, part = threadIdx.x % G;
   const uint64_t mine = me < n ? s.list[me] : kSmAll;
   const float x = sm_place_value(mine);
   int b;
   const uint64_t w = me < n ? sm_weight(x, r, s.table, b) : 0ull;
-  s.m0[me] = w;
+  if (part == 0 && me < n) s.m0[me] = w;
   __syncthreads();
   uint32_t before = 0;
   uint64_t mass = 0;
 #pragma unroll 4
-  for (uint32_t j = 0; j < n; ++j)
+  for (uint32_t j = part; j < n; j += G)
     if (s.list[j] < mine) ++before, mass += s.m0[j];
-  const uint64_t wk = before < (uint32_t)k ? w : 0ull;
-  const uint64_t whole = sum_all(wk);       // (its barriers also end the reading of m0)
-  const bool kept = wk > 0 && wk >= least && (before == 0 || (double)mass < (double)p * (double)whole || p >= 1.f);
-  s.m0[me] = kept ? w : 0ull;
-  const uint64_t total = sum_all(kept ? w : 0ull);
+  for (int o = 1; o < G; o <<= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    mass += __shfl_xor_sync(0xffffffffu, mass, o);
+  }
+  const uint64_t wk = before < k ? w : 0ull;
+  const uint64_t in_k = sum_all(part == 0 ? wk : 0ull);   // (its barriers also end the reading of m0)
+  if (whole == 0) whole = in_k;
+  const bool kept = wk > 0 && wk >= least && (before == 0 || p >= 1.f || (double)mass < (double)p * (double)whole);
+  if (part == 0 && me < n) s.m0[me] = kept ? w : 0ull;
+  const uint64_t total = sum_all(part == 0 && kept ? w : 0ull);
   const uint64_t target = min((uint64_t)(u * (double)total), total - 1);
-  if (!kept) return;
   uint64_t run = 0;
 #pragma unroll 4
-  for (uint32_t j = 0; j < n; ++j)
+  for (uint32_t j = part; j < n; j += G)
     if ((uint32_t)s.list[j] < (uint32_t)mine) run += s.m0[j];
-  if (run <= target && run + w > target) {
+  for (int o = 1; o < G; o <<= 1) run += __shfl_xor_sync(0xffffffffu, run, o);
+  if (kept && part == 0 && run <= target && run + w > target) {
     a.ids[rw] = (int32_t)(uint32_t)mine;
     if (a.prob) a.prob[rw] = sm_prob(x, r, s.table, t, total);
   }
@@ -700,7 +710,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
       z.pick(true, (uint32_t)k, 0.0, 0ull, 0u);
       const uint32_t n = s.above_cnt + s.bin_cnt;
       if (s.bin < kSmBins && n <= (uint32_t)THREADS) {
-        z.few(s.bin, n, k, p, sm_min_weight(mp), un, from, a, rw, t);
+        z.few(s.bin, n, (uint32_t)k, 0ull, p, sm_min_weight(mp), un, from, a, rw, t);
         return;
       }
       border = z.find(true, (uint32_t)k, 0.0, from, border);
@@ -709,6 +719,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
     if (p < 1.f) {
       z.clear();
       const uint32_t il = (uint32_t)border;
+      // rows in shared memory are short: there it pays to count as well, for few()
+      const bool count = RES && border == kSmAll;
       z.each(from, [&](const float (&x)[4], uint32_t i) {
         uint64_t w[4];
         int bin[4];
@@ -716,7 +728,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
         if (border == kSmAll) {             // (the usual case, kept short: this pass is bound by issue)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (x[e] >= from) z.add(&s.h.lo[bin[e]], &s.h.hi[bin[e]], w[e]);
+            if (x[e] >= from) {
+              z.add(&s.h.lo[bin[e]], &s.h.hi[bin[e]], w[e]);
+              if (count) atomicAdd(&s.h.cnt[bin[e]], 1u);
+            }
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -724,7 +739,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
               z.add(&s.h.lo[bin[e]], &s.h.hi[bin[e]], w[e]);
         }
       });
-      z.exchange(true, false);
+      z.exchange(true, count);
       uint64_t whole = 0, m = 0;
       for (int b = tid; b < kSmBins; b += THREADS) m += s.m0[b];
 #pragma unroll
@@ -734,6 +749,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
       for (int q = 0; q < Sm::W; ++q) whole += s.wsum[q];
       __syncthreads();
       z.pick(false, 0u, (double)p * (double)whole, 0ull, 0u);
+      const uint32_t n = s.above_cnt + s.bin_cnt;
+      if (count && n <= (uint32_t)THREADS) {
+        z.few(s.bin, n, UINT32_MAX, whole, p, sm_min_weight(mp), un, from, a, rw, t);
+        return;
+      }
       border = z.find(false, 0u, (double)p * (double)whole, from, border);
       if (border != kSmAll) from = fmaxf(from, sm_place_value(border));
     }
