@@ -111,6 +111,7 @@ __global__ void __launch_bounds__(kMxThreads)
                       uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   using P = MxPiece<T>;
   constexpr int LB = 32 / P::N, U = 2;      // lanes a block, pieces in flight
+  ptx::grid_release();                      // (scores of these codes may set themselves up)
   MxPieces p(nb * LB);
   const int64_t rows = (n + 127) / 128 * 128;   // rows behind the last only have scales, 0
   // (whole warps stay together for the exchange: a warp leaves when its first piece is behind the end)
@@ -482,6 +483,7 @@ __global__ void __launch_bounds__(MxEpi<NT>::kThreads, MxCfg<NT, KB>::kCtas)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = bars->tmem;
+  ptx::grid_wait();
 
   if (warp == 0) {
     {
@@ -626,6 +628,7 @@ __global__ void __launch_bounds__(MxPackCfg<NT, KB>::kThreads, MxPackCfg<NT, KB>
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = bars->tmem;
+  ptx::grid_wait();
 
   if (warp == 0) {
     {
@@ -849,6 +852,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxPairCfg<T>::kThrea
   ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem = bars->tmem;
+  ptx::grid_wait();
   auto timeout = [&] {
     if (status) atomicCAS(status, FGMM_OK, FGMM_ERR_TIMEOUT);
     bars->abort = 1;
@@ -1061,6 +1065,22 @@ struct MxArgs {
   cudaStream_t s;
 };
 
+// Launch that may begin before the encoding of the queries has ended (grid_wait in the kernels).
+template <typename... P, typename... A>
+cudaError_t mx_launch(void (*kernel)(P...), unsigned grid, int threads, int smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // Grid and attributes of a kernel with configuration C; its query and vector tiles.
 template <typename C, typename K>
 cudaError_t mx_grid_of(K* kernel, int64_t tiles, unsigned* grid) {
@@ -1092,19 +1112,18 @@ cudaError_t mx_scores(const MxArgs& a) {
     const int64_t steps = (vt + C::kSub - 1) / C::kSub;
     auto* k = mx4_scores_packed_kernel<NT, KB, T>;
     if ((e = mx_grid_of<C>(k, steps * qt, &grid)) != cudaSuccess) return e;
-    k<<<grid, C::kThreads, C::kSmem, a.s>>>(tmq, a.xc, a.xs, a.qs, a.n, a.m, a.nb, steps, qt, a.alpha, a.bias,
-                                            static_cast<T*>(a.out), a.ldo, a.status);
-    return cudaGetLastError();
+    return mx_launch(k, grid, C::kThreads, C::kSmem, a.s, tmq, a.xc, a.xs, a.qs, a.n, a.m, a.nb, steps, qt,
+                     a.alpha, a.bias, static_cast<T*>(a.out), a.ldo, a.status);
   }
   if constexpr (kBoxes) {
     using C = MxCfg<NT, KB>;
     auto* k = mx4_scores_kernel<NT, KB, T>;
     if ((e = mx_grid_of<C>(k, vt * qt, &grid)) != cudaSuccess) return e;
     if (!mx_tmap(&tmx, a.xc, a.nb, a.n, KB, kMxBM)) return cudaErrorInvalidValue;
-    k<<<grid, C::kThreads, C::kSmem, a.s>>>(tmx, tmq, a.xs, a.qs, a.n, a.m, a.nb, vt, qt, a.alpha, a.bias,
-                                            static_cast<T*>(a.out), a.ldo, a.status);
+    e = mx_launch(k, grid, C::kThreads, C::kSmem, a.s, tmx, tmq, a.xs, a.qs, a.n, a.m, a.nb, vt, qt, a.alpha,
+                  a.bias, static_cast<T*>(a.out), a.ldo, a.status);
   }
-  return cudaGetLastError();
+  return e;
 }
 
 template <typename T>
@@ -1122,9 +1141,8 @@ cudaError_t mx_scores_pair(const MxArgs& a) {
   if (e != cudaSuccess) return e;
   const int64_t vp = (a.n + 2 * kMxBM - 1) / (2 * kMxBM), qt = (a.m + C::NT - 1) / C::NT;
   const int64_t pairs = vp * qt < sms / 2 ? vp * qt : sms / 2;
-  k<<<(unsigned)(2 * pairs), C::kThreads, C::kSmem, a.s>>>(tmx, tmq, tmxs, tmqs, a.n, a.m, a.nb, vp, qt, a.alpha,
-                                                           a.bias, static_cast<T*>(a.out), a.ldo, a.status);
-  return cudaGetLastError();
+  return mx_launch(k, (unsigned)(2 * pairs), C::kThreads, C::kSmem, a.s, tmx, tmq, tmxs, tmqs, a.n, a.m, a.nb,
+                   vp, qt, a.alpha, a.bias, static_cast<T*>(a.out), a.ldo, a.status);
 }
 
 template <int KB, typename T>
