@@ -442,8 +442,9 @@ int fgmm_ivf_search(int K, int D, const float* centroids, const int64_t* offsets
  *
  * fgmm_mx4_scores: out[m][n] = alpha * sum_d q[m][d] x[n][d] + bias[n] for codes of M queries and
  * of N vectors of the same D (the padding adds 0); bias: optional device float[N] (-|x|^2 / 2
- * ranks by L2 distance).  Products and sums are fp32; out_dtype FGMM_F32 or FGMM_BF16, rows of
- * stride ldo >= N.  status: optional device int, set to FGMM_ERR_TIMEOUT if a bounded wait of the
+ * ranks by L2 distance).  Products are exact, sums are fp32 (what is below 2^-126 may come out as
+ * 0, what is above the largest fp32 as infinity); out_dtype FGMM_F32 or FGMM_BF16, rows of stride
+ * ldo >= N.  status: optional device int, set to FGMM_ERR_TIMEOUT if a bounded wait of the
  * kernel expires (the output is then undefined), else left as it is. */
 #define FGMM_MX4_MAX_ROWS ((1ll << 31) - 1024)
 #define FGMM_MX4_MAX_D (1 << 20)
@@ -479,7 +480,7 @@ int fgmm_mx4_scores(const uint8_t* q_codes, const uint8_t* q_scales, int64_t M,
  * parameter outside its range, gives id -1 and prob NaN; where some logits are +inf, they have
  * weight 1 and all others 0.  Decisions do not depend on the order of summation: weights are
  * held as 64-bit integers, exp rounded to 2^-40 of the largest weight (a token below 2^-41 of it
- * is not drawn), and all sums are exact.  V <= FGMM_SAMPLE_MAX_V (FGMM_ERR_UNSUPPORTED above);
+ * is not drawn), all sums are exact, and all comparisons are of these.  V <= FGMM_SAMPLE_MAX_V (FGMM_ERR_UNSUPPORTED above);
  * rows = 0 does nothing. */
 #define FGMM_SAMPLE_MAX_V (1 << 22)
 int fgmm_sample_logits(const void* logits, int dtype, int64_t rows, int V, int64_t ld,

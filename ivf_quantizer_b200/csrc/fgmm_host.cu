@@ -182,6 +182,8 @@ int map_cuda(cudaError_t e) {
   return FGMM_ERR_CUDA;
 }
 
+// A pointer (NULL allowed) to elements of `size` bytes that they may be read or written at.
+bool at_element(const void* p, size_t size) { return (uintptr_t)p % size == 0; }
 // Codes and scales as every fgmm_mx4 call wants them.
 bool mx4_aligned(const uint8_t* codes, const uint8_t* scales) {
   return codes && scales && ((uintptr_t)codes | (uintptr_t)scales) % 16 == 0;
@@ -1063,7 +1065,7 @@ int fgmm_mx4_encode(const void* X, int x_dtype, int64_t N, int D, int64_t ldx, u
     return FGMM_ERR_INVALID_ARG;
   if (N > FGMM_MX4_MAX_ROWS || D > FGMM_MX4_MAX_D) return FGMM_ERR_UNSUPPORTED;
   if (N == 0) return FGMM_OK;
-  if (!X || !mx4_aligned(codes, scales) || (uintptr_t)X % (x_dtype == FGMM_F32 ? 4 : 2))
+  if (!X || !mx4_aligned(codes, scales) || !at_element(X, x_dtype == FGMM_F32 ? 4 : 2))
     return FGMM_ERR_INVALID_ARG;
   return map_cuda(launch_mx4_encode(X, x_dtype, N, D, ldx, codes, scales, (cudaStream_t)stream));
 }
@@ -1074,7 +1076,7 @@ int fgmm_mx4_decode(const uint8_t* codes, const uint8_t* scales, int64_t N, int 
     return FGMM_ERR_INVALID_ARG;
   if (N > FGMM_MX4_MAX_ROWS || D > FGMM_MX4_MAX_D) return FGMM_ERR_UNSUPPORTED;
   if (N == 0) return FGMM_OK;
-  if (!out || !mx4_aligned(codes, scales) || (uintptr_t)out % (out_dtype == FGMM_F32 ? 4 : 2))
+  if (!out || !mx4_aligned(codes, scales) || !at_element(out, out_dtype == FGMM_F32 ? 4 : 2))
     return FGMM_ERR_INVALID_ARG;
   return map_cuda(launch_mx4_decode(codes, scales, N, D, out, out_dtype, ldo,
                                     (cudaStream_t)stream));
@@ -1090,7 +1092,7 @@ int fgmm_mx4_scores(const uint8_t* q_codes, const uint8_t* q_scales, int64_t M,
     return FGMM_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return FGMM_OK;
   if (!out || !mx4_aligned(q_codes, q_scales) || !mx4_aligned(codes, scales) ||
-      (uintptr_t)out % (out_dtype == FGMM_F32 ? 4 : 2) || (uintptr_t)bias % 4)
+      !at_element(out, out_dtype == FGMM_F32 ? 4 : 2) || !at_element(bias, 4) || !at_element(status, 4))
     return FGMM_ERR_INVALID_ARG;
   return map_cuda(launch_mx4_scores(q_codes, q_scales, M, codes, scales, N, D, alpha, bias, out,
                                     out_dtype, ldo, status, (cudaStream_t)stream));
@@ -1104,7 +1106,9 @@ int fgmm_sample_logits(const void* logits, int dtype, int64_t rows, int V, int64
     return FGMM_ERR_INVALID_ARG;
   if (V > FGMM_SAMPLE_MAX_V || rows > INT32_MAX) return FGMM_ERR_UNSUPPORTED;
   if (rows == 0) return FGMM_OK;
-  if (!logits || !u || !ids || (uintptr_t)logits % (dtype == FGMM_F32 ? 4 : 2))
+  if (!logits || !u || !ids || !at_element(logits, dtype == FGMM_F32 ? 4 : 2) || !at_element(u, 8) ||
+      !at_element(ids, 4) || !at_element(prob, 4) || !at_element(temperature, 4) ||
+      !at_element(top_k, 4) || !at_element(top_p, 4) || !at_element(min_p, 4))
     return FGMM_ERR_INVALID_ARG;
   return map_cuda(launch_sample_logits(logits, dtype, rows, V, ld, temperature, top_k, top_p,
                                        min_p, u, ids, prob, (cudaStream_t)stream));

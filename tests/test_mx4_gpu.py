@@ -229,3 +229,58 @@ def test_offsets_beyond_32_bits():
     s = m.scores(qs, dtype=torch.bfloat16)
     ref = q.MX4(tail).scores(qs, dtype=torch.bfloat16)
     assert torch.equal(s[:, -64:], ref) and (s[-1, :1000] == 0).all()
+
+
+def test_scores_at_random_shapes():
+    """Every kernel and its ragged edges: few and many queries, short and long rows, any N."""
+    import ivf_quantizer_b200 as q
+    rng = np.random.default_rng(19)
+    for i in range(60):
+        m = int(np.exp(rng.uniform(0, np.log(600))))
+        n = int(np.exp(rng.uniform(0, np.log(4000))))
+        d = int(np.exp(rng.uniform(0, np.log(1500))))
+        dt = (torch.float32, torch.bfloat16)[i % 2]
+        qs, x = _x(m, d, i, dt).cuda(), _x(n, d, i + 100).cuda()
+        bias = torch.randn(n, device="cuda") if i % 3 == 0 else None
+        got = q.MX4(x).scores(qs, alpha=-0.5, bias=bias, dtype=(torch.float32, torch.bfloat16)[i // 2 % 2])
+        _check_scores(got, qs, x, -0.5, bias, d)
+
+
+def test_scores_of_very_small_values_lose_at_most_the_smallest_normal():
+    import ivf_quantizer_b200 as q
+    qs, x = _x(20, 300, 20).cuda() * 2.0 ** -70, _x(200, 300, 21).cuda() * 2.0 ** -58
+    got = _np(q.MX4(x).scores(qs))
+    qv, xv = (M.decode(*M.encode(_np(t)), 300) for t in (qs, x))
+    want, mag = M.scores(qv, xv)
+    assert np.isfinite(got).all() and (np.abs(got - want) <= 302 * 2.0 ** -24 * mag + 300 * 2.0 ** -126).all()
+
+
+def test_non_finite_queries_spoil_their_row_alone():
+    import ivf_quantizer_b200 as q
+    x, qs = _x(300, 200, 22).cuda(), _x(70, 200, 23).cuda()
+    index = q.MX4(x)
+    want = index.scores(qs)
+    qs[5, 7], qs[69, 199] = float("nan"), float("inf")
+    got = index.scores(qs)
+    bad = torch.zeros(70, dtype=torch.bool)
+    bad[[5, 69]] = True
+    assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], want[~bad])
+
+
+def test_two_streams_at_once():
+    """Kernels of different tile sizes side by side: they share the SMs' tensor memory."""
+    import ivf_quantizer_b200 as q
+    x, y = q.MX4(_x(6000, 600, 24).cuda()), q.MX4(_x(9000, 96, 25).cuda())
+    calls = [(x, _x(300, 600, 26).cuda()), (y, _x(3, 96, 27).cuda()), (x, _x(20, 600, 28).cuda()),
+             (y, _x(200, 96, 29).cuda())]
+    want = [a.scores(b) for a, b in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    got = [[] for _ in calls]
+    for _ in range(10):
+        for s, g, (a, b) in zip(streams, got, calls):
+            with torch.cuda.stream(s):
+                g.append(a.scores(b))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(o, w) for o in g)

@@ -110,6 +110,13 @@ def test_abi_refusals():
     assert sa(p, 9, 2, 4, 4, z, z, z, z, p, p, z, z) == bad
     assert sa(p, 0, 2, 4, 4, z, z, z, z, z, p, z, z) == bad               # no uniforms
     assert sa(p, 0, 2, 4, 4, z, z, z, z, p, z, z, z) == bad               # no ids
+    two = ctypes.c_void_p(66)
+    for i in range(5, 12):                                               # pointers off their elements
+        args = [p, 0, 2, 4, 4, z, z, z, z, p, p, z, z]
+        args[i] = two
+        assert sa(*args) == bad, i
+    assert sa(two, 0, 2, 4, 4, z, z, z, z, p, p, z, z) == bad
+    assert sc(p, p, 2, p, p, 4, 4, one, z, p, 0, 4, two, z) == bad        # the status word
     assert sa(p, 0, 2, (1 << 22) + 1, 1 << 23, z, z, z, z, p, p, z, z) == uns
 
 

@@ -243,3 +243,21 @@ def test_queries_scored_on_codes_and_drawn():
     g.close()
     # the points' own rounding to 4 bits moves some of them to a neighbour, not most
     assert (hard[:, 0] == greedy).float().mean().item() > 0.5
+
+
+def test_draws_at_random_shapes_and_settings():
+    rng = np.random.default_rng(23)
+    for i in range(60):
+        rows, v = int(rng.integers(1, 6)), int(np.exp(rng.uniform(0, np.log(70000))))
+        g = torch.Generator().manual_seed(1000 + i)
+        x = torch.randn(rows, v, generator=g) * float(rng.choice([0.05, 1.0, 3.0, 20.0]))
+        x[torch.rand(rows, v, generator=g) < float(rng.choice([0.0, 0.5]))] = -float("inf")
+        if i % 4 == 0:
+            x = torch.round(x * 2) / 2                   # many ties
+        x[:, int(rng.integers(0, v))] = 2.0
+        t, k, p, m, u = _params(rows, v, 2000 + i)
+        if i % 3 == 0:
+            k = torch.randint(0, v + 1, (rows,), generator=g, dtype=torch.int32).cuda()
+        use = int(rng.integers(0, 8))
+        dt = (torch.float32, torch.bfloat16)[i % 2]
+        _check(x.to(dt).cuda(), u, t, k if use & 1 else None, p if use & 2 else None, m if use & 4 else None)
