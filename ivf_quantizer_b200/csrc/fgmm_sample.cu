@@ -167,7 +167,7 @@ __device__ __forceinline__ float sm_prob(float x, const SmRow& r, const double* 
   return (float)(p * e / (double)total);
 }
 
-constexpr int kSmList = 2048;               // tokens of a border bin that are sorted
+constexpr int kSmList = kSmBins * 12 / 8;    // tokens of a border bin that are ranked: what a histogram's room holds
 
 template <int THREADS>
 struct SmShared {
@@ -176,7 +176,7 @@ struct SmShared {
   // this CTA's histogram (mass in two words, number); then, in CTA 0, the list that is sorted
   union {
     struct { uint32_t lo[kSmBins], hi[kSmBins], cnt[kSmBins]; } h;
-    uint64_t list[THREADS < 512 ? 1024 : kSmList];
+    uint64_t list[kSmList];
   };
   uint64_t m0[kSmBins];                     // the cluster's
   uint32_t c0[kSmBins];
@@ -1006,9 +1006,12 @@ cudaError_t sm_choose(SmArgs a, int64_t rows, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  constexpr int kSmall = 128, kLarge = 512;
+  // threads: a row of up to 4096 tokens; slices in shared memory, two CTAs a SM; slices in place, four
+  // (more rows side by side cover one another's barriers: 173 us against 182, 256 x 131072)
+  constexpr int kSmall = 128, kLarge = 512, kLong = 256;
   constexpr size_t kFixedSmall = (sizeof(SmShared<kSmall>) + 15) / 16 * 16;
   constexpr size_t kFixed = (sizeof(SmShared<kLarge>) + 15) / 16 * 16;
+  constexpr size_t kFixedLong = (sizeof(SmShared<kLong>) + 15) / 16 * 16;
   constexpr size_t kHalf = 113 * 1024;      // two CTAs a SM
   const auto bytes = [&](int C) { return ((size_t)((a.V + C - 1) / C) * sizeof(T) + 31) / 16 * 16; };
   if (a.V <= kSmWarpV && !a.top_k && !a.top_p) {
@@ -1019,13 +1022,15 @@ cudaError_t sm_choose(SmArgs a, int64_t rows, cudaStream_t st) {
     a.slice = a.V;
     return sm_launch<T, kSmall, true>(a, rows, 1, kFixedSmall + bytes(1), st);
   }
+  // CTAs a row: while the rows leave SMs idle, and until a slice has at most 32768 tokens (a row of
+  // 131072 by one CTA 228 us, by two 208, by four 199, by eight 244, at 256 rows)
   int C = 1;
   while (C < 8 && (a.V / C > 32768 || (rows * C < sms && a.V / C > 4096))) C *= 2;
   a.slice = (a.V + C - 1) / C;
   if (rows * C > INT32_MAX) return cudaErrorInvalidValue;
   if (kFixed + bytes(C) <= kHalf)
     return sm_launch<T, kLarge, true>(a, rows, C, kFixed + bytes(C), st);
-  return sm_launch<T, kLarge, false>(a, rows, C, kFixed, st);
+  return sm_launch<T, kLong, false>(a, rows, C, kFixedLong, st);
 }
 
 }  // namespace
