@@ -309,6 +309,14 @@ struct Sampler {
   __device__ void exchange(bool mass, bool count) {
     sync();
     if (threadIdx.x == 0) s.nlist = s.nfew = 0u;
+    if (C == 1) {
+      for (int b = threadIdx.x; b < kSmBins; b += THREADS) {
+        s.m0[b] = ((uint64_t)s.h.hi[b] << 32) + s.h.lo[b];
+        s.c0[b] = s.h.cnt[b];
+      }
+      __syncthreads();
+      return;
+    }
     const int seg = kSmBins / C;
     for (int i = threadIdx.x; i < seg; i += THREADS) {
       const int b = rank * seg + i;
@@ -333,14 +341,10 @@ struct Sampler {
   // kSmBins if none does), what is before it and how many tokens it holds.
   __device__ void pick(bool by_count, uint32_t k, double need, uint64_t above_mass, uint32_t above_cnt) {
     constexpr int PER = (kSmBins + THREADS - 1) / THREADS;
-    uint64_t mass[PER], msum = 0;
-    uint32_t cnt[PER], csum = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int b = threadIdx.x * PER + i;
-      mass[i] = b < kSmBins ? s.m0[b] : 0ull, cnt[i] = b < kSmBins ? s.c0[b] : 0u;
-      msum += mass[i], csum += cnt[i];
-    }
+    const int b0 = threadIdx.x * PER, b1 = min(b0 + PER, kSmBins);
+    uint64_t msum = 0;
+    uint32_t csum = 0;
+    for (int b = b0; b < b1; ++b) msum += s.m0[b], csum += s.c0[b];
     uint64_t mi = msum;
     uint32_t ci = csum;
 #pragma unroll
@@ -364,14 +368,13 @@ struct Sampler {
     mi += __shfl_sync(0xffffffffu, before, 0), ci += __shfl_sync(0xffffffffu, cbefore, 0);
     uint64_t run_m = above_mass + mi - msum;
     uint32_t run_c = above_cnt + ci - csum;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
+    for (int b = b0; b < b1; ++b) {
       const bool was = by_count ? run_c >= k : (double)run_m >= need;
-      const uint64_t nm = run_m + mass[i];
-      const uint32_t nc = run_c + cnt[i];
+      const uint64_t nm = run_m + s.m0[b];
+      const uint32_t nc = run_c + s.c0[b];
       if (!was && (by_count ? nc >= k : (double)nm >= need)) {
-        s.bin = threadIdx.x * PER + i;
-        s.bin_cnt = cnt[i];
+        s.bin = b;
+        s.bin_cnt = nc - run_c;
         s.above_mass = run_m;
         s.above_cnt = run_c;
       }
@@ -958,26 +961,35 @@ __global__ void __launch_bounds__(32 * kSmWarps) sample_warp_kernel(const SmArgs
     const uint64_t w = t == 0.f ? 1ull : sm_weight((float)val[kept[j]], r, table, bin);
     return w >= least ? w : 0ull;
   };
-  uint64_t total = 0;
-  for (int j = lane; j < n; j += 32) total += weight(j);
+  // a contiguous run of the list a lane; then the lane whose run holds the target, by the whole warp
+  const int per = (n + 31) / 32;
+  uint64_t sum = 0;
+  for (int i = 0, at = per > 0 ? lane % per : 0; i < per; ++i) {   // (starts apart: no two lanes on a bank)
+    sum += weight(lane * per + at);
+    if (++at == per) at = 0;
+  }
+  uint64_t inc = sum;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t b = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += b;
+  }
+  const uint64_t total = __shfl_sync(0xffffffffu, inc, 31);
   const uint64_t target = t == 0.f ? 0ull : min((uint64_t)(un * (double)total), total - 1);
-  uint64_t run = 0;
-  for (int j0 = 0; j0 < n && run <= target; j0 += 32) {
-    const uint64_t w = weight(j0 + lane);
-    uint64_t inc = w;
+  const int owner = __ffs(__ballot_sync(0xffffffffu, inc > target)) - 1;
+  const uint64_t before = __shfl_sync(0xffffffffu, inc - sum, owner);
+  const int j = owner * per + lane;
+  const uint64_t w = lane < per ? weight(j) : 0ull;
+  inc = w;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t b = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += b;
-    }
-    if (run + inc > target && run + inc - w <= target) {
-      const int i = kept[j0 + lane];
-      a.ids[rw] = i;
-      if (a.prob) a.prob[rw] = sm_prob((float)val[i], r, table, t, total);
-    }
-    run += __shfl_sync(0xffffffffu, inc, 31);
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t b = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += b;
+  }
+  if (w > 0 && before + inc > target && before + inc - w <= target) {
+    const int i = kept[j];
+    a.ids[rw] = i;
+    if (a.prob) a.prob[rw] = sm_prob((float)val[i], r, table, t, total);
   }
 }
 
