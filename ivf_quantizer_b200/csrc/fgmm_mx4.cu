@@ -104,14 +104,14 @@ __device__ __forceinline__ int64_t mx_scale_at(int64_t row, int b, int nkc) {
 // A thread encodes 32 bytes of a row at a time, four (fp32) or two (bf16) neighbouring lanes a block;
 // codes lie in the order of the threads, so a warp writes them as one contiguous piece.  Two pieces a
 // thread are loaded before either is used.  Bound by memory; a lane a 4 values took
-// 1266 us at 10^6 x 960 bf16 (issue), this takes MEASURE.  VEC: rows allow 16-byte loads.
+// 1266 us at 10^6 x 960 bf16 (issue), this takes 440.  VEC: rows allow 16-byte loads.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kMxThreads)
     mx4_encode_kernel(const T* __restrict__ X, int64_t n, int D, int64_t ldx, int nb, int nkc,
                       uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   using P = MxPiece<T>;
   constexpr int LB = 32 / P::N, U = 2;      // lanes a block, pieces in flight
-  ptx::grid_release();                      // (scores of these codes may set themselves up)
+  ptx::grid_release();                      // (kernels that read these codes may set themselves up)
   MxPieces p(nb * LB);
   const int64_t rows = (n + 127) / 128 * 128;   // rows behind the last only have scales, 0
   // (whole warps stay together for the exchange: a warp leaves when its first piece is behind the end)
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kMxThreads)
 // r + 64, r + 96 of a 128-row tile: 16 bytes a lane and row, and the four rows' scales of a block lie
 // in the same 16 bytes of the scale tile.  Bound by writing; with the encoder's mapping (a flat
 // sequence of pieces) the address arithmetic of every 16 bytes took it to 979 us at 10^6 x 960 fp32,
-// against MEASURE.
+// against 685.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kMxThreads)
     mx4_decode_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(kMxThreads)
                       int64_t ldo) {
   constexpr int N = 16 / sizeof(T);
   using Codes = std::conditional_t<N == 4, uint16_t, uint32_t>;
+  ptx::grid_wait();
   const int lane = threadIdx.x & 31;
   const int64_t step = (int64_t)gridDim.x * (kMxThreads / 32);
   for (int64_t g = (int64_t)blockIdx.x * (kMxThreads / 32) + (threadIdx.x >> 5); g < groups; g += step) {
@@ -1065,7 +1066,7 @@ struct MxArgs {
   cudaStream_t s;
 };
 
-// Launch that may begin before the encoding of the queries has ended (grid_wait in the kernels).
+// Launch that may begin before the encoding of its operands has ended (grid_wait in the kernels).
 template <typename... P, typename... A>
 cudaError_t mx_launch(void (*kernel)(P...), unsigned grid, int threads, int smem, cudaStream_t s, A... args) {
   cudaLaunchConfig_t cfg = {};
@@ -1200,13 +1201,12 @@ cudaError_t launch_mx4_decode(const uint8_t* codes, const uint8_t* scales, int64
   const unsigned grid = (unsigned)(blocks < (1 << 30) ? blocks : (1 << 30));
   if (out_dtype == FGMM_F32) {
     auto* k = vec ? mx4_decode_kernel<float, true> : mx4_decode_kernel<float, false>;
-    k<<<grid, kMxThreads, 0, s>>>(codes, scales, n, D, nb, nkc, nkg, groups, static_cast<float*>(out), ldo);
-  } else {
-    auto* k = vec ? mx4_decode_kernel<__nv_bfloat16, true> : mx4_decode_kernel<__nv_bfloat16, false>;
-    k<<<grid, kMxThreads, 0, s>>>(codes, scales, n, D, nb, nkc, nkg, groups,
-                                  static_cast<__nv_bfloat16*>(out), ldo);
+    return mx_launch(k, grid, kMxThreads, 0, s, codes, scales, n, D, nb, nkc, nkg, groups,
+                     static_cast<float*>(out), ldo);
   }
-  return cudaGetLastError();
+  auto* k = vec ? mx4_decode_kernel<__nv_bfloat16, true> : mx4_decode_kernel<__nv_bfloat16, false>;
+  return mx_launch(k, grid, kMxThreads, 0, s, codes, scales, n, D, nb, nkc, nkg, groups,
+                   static_cast<__nv_bfloat16*>(out), ldo);
 }
 
 cudaError_t launch_mx4_scores(const uint8_t* q_codes, const uint8_t* q_scales, int64_t m,

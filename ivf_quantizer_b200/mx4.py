@@ -15,6 +15,13 @@ _DTYPES = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16}
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
+def empty(n: int, d: int | None, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+    """[n, d], or [n] without d (torch.empty takes half as long again)."""
+    if d is not None:
+        return torch.empty_strided((n, d), (d, 1), dtype=dtype, device=device)
+    return torch.empty_strided((n,), (1,), dtype=dtype, device=device)
+
+
 def call(fn, name: str, device: torch.device, *args) -> None:
     """fn(*args, current stream of `device`) with `device` as the current one."""
     i = device.index
@@ -53,8 +60,8 @@ class MX4:
         dt, N, D, ldx = _rows(X, "X")
         dev, nb = X.device, -(-D // _lib.MX4_BLOCK)
         self.shape = (N, D)
-        self.codes = torch.empty((N, nb * 16), dtype=torch.uint8, device=dev)
-        self.scales = torch.empty(-(-N // 128) * -(-nb // 4) * 512, dtype=torch.uint8, device=dev)
+        self.codes = empty(N, nb * 16, torch.uint8, dev)
+        self.scales = empty(-(-N // 128) * -(-nb // 4) * 512, None, torch.uint8, dev)
         call(LIB.fgmm_mx4_encode, "fgmm_mx4_encode", dev, X.data_ptr(), dt, N, D, ldx,
              self.codes.data_ptr(), self.scales.data_ptr())
 
@@ -82,7 +89,7 @@ class MX4:
             raise TypeError("dtype must be float32 or bfloat16")
         N, D = self.shape
         dev = self.codes.device
-        out = torch.empty((N, D), dtype=dtype, device=dev)
+        out = empty(N, D, dtype, dev)
         call(LIB.fgmm_mx4_decode, "fgmm_mx4_decode", dev, self.codes.data_ptr(),
              self.scales.data_ptr(), N, D, out.data_ptr(), _DTYPES[dtype], D)
         return out
@@ -91,20 +98,36 @@ class MX4:
                dtype: torch.dtype = torch.float32) -> torch.Tensor:
         """alpha * queries @ rows.T + bias, [M, N].  queries: an MX4, or a [M, D] tensor, which
         is encoded first.  bias: float32 [N]."""
-        q = queries if isinstance(queries, MX4) else MX4(queries)
-        (M, D), N = q.shape, self.shape[0]
-        if D != self.shape[1]:
-            raise ValueError(f"queries have {D} dimensions, the codes {self.shape[1]}")
+        N, D = self.shape
         dev = self.codes.device
-        if q.codes.device != dev:
+        coded = isinstance(queries, MX4)
+        if coded:
+            (M, d), q_dev = queries.shape, queries.codes.device
+        else:
+            dt, M, d, ldq = _rows(queries, "queries")
+            q_dev = queries.device
+        if d != D:
+            raise ValueError(f"queries have {d} dimensions, the codes {D}")
+        if q_dev != dev:
             raise ValueError("queries and codes must be on one device")
-        if dtype not in _DTYPES:
+        out_dt = _DTYPES.get(dtype)
+        if out_dt is None:
             raise TypeError("dtype must be float32 or bfloat16")
         if bias is not None and not (bias.device == dev and bias.dtype == torch.float32
                                      and bias.shape == (N,) and bias.is_contiguous()):
             raise ValueError("bias must be a contiguous float32 [N] tensor on the codes' device")
-        out = torch.empty((M, N), dtype=dtype, device=dev)
-        call(LIB.fgmm_mx4_scores, "fgmm_mx4_scores", dev, q.codes.data_ptr(), q.scales.data_ptr(), M,
-             self.codes.data_ptr(), self.scales.data_ptr(), N, D, alpha,
-             None if bias is None else bias.data_ptr(), out.data_ptr(), _DTYPES[dtype], N, None)
+        if coded:
+            q_codes, q_scales = queries.codes.data_ptr(), queries.scales.data_ptr()
+        else:
+            nb = -(-D // _lib.MX4_BLOCK)
+            split = -(-M * nb // 32) * 512    # (copies of scale tiles want their own 512 bytes)
+            scratch = empty(split + -(-M // 128) * -(-nb // 4) * 512, None, torch.uint8, dev)
+            q_codes = scratch.data_ptr()
+            q_scales = q_codes + split
+            call(LIB.fgmm_mx4_encode, "fgmm_mx4_encode", dev, queries.data_ptr(), dt, M, D, ldq,
+                 q_codes, q_scales)
+        out = empty(M, N, dtype, dev)
+        call(LIB.fgmm_mx4_scores, "fgmm_mx4_scores", dev, q_codes, q_scales, M, self.codes.data_ptr(),
+             self.scales.data_ptr(), N, D, alpha, None if bias is None else bias.data_ptr(),
+             out.data_ptr(), out_dt, N, None)
         return out

@@ -5,7 +5,7 @@ from __future__ import annotations
 import torch
 
 from ._lib import LIB
-from .mx4 import _rows, call
+from .mx4 import _rows, call, empty
 
 
 def _per_row(v, name, dtype, rows, device):
@@ -41,8 +41,8 @@ def sample_logits(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k
     top_k = _per_row(top_k, "top_k", torch.int32, rows, dev)
     top_p = _per_row(top_p, "top_p", torch.float32, rows, dev)
     min_p = _per_row(min_p, "min_p", torch.float32, rows, dev)
-    ids = torch.empty(rows, dtype=torch.int32, device=dev)
-    prob = torch.empty(rows, dtype=torch.float32, device=dev)
+    ids = empty(rows, None, torch.int32, dev)
+    prob = empty(rows, None, torch.float32, dev)
     call(LIB.fgmm_sample_logits, "fgmm_sample_logits", dev, logits.data_ptr(), dt, rows, V, ld,
          *[None if t is None else t.data_ptr() for t in (temperature, top_k, top_p, min_p)],
          u.data_ptr(), ids.data_ptr(), prob.data_ptr())
