@@ -236,16 +236,16 @@ __global__ void __launch_bounds__(kMxThreads)
 // queries the N side (NT a tile: TMEM column = query).  The codes then stream through the wide
 // side whatever the number of queries, and a warp holds 32 consecutive scores of one query.
 //
-// A CTA walks its tiles: a producer thread fills a ring of stages (KB bytes of each of 128 vectors
-// and their scale tiles), one thread copies a stage's scales to TMEM and issues its K = 64
-// block-scaled products, and the epilogue warps drain one of two accumulators while the other is
-// filled.  Two kernels differ in how a stage is filled:
+// A CTA walks its tiles: a producer warp fills a ring of stages (KB bytes of each of 128 vectors and
+// their scale tiles), another copies a stage's scales to TMEM and issues its K = 64 block-scaled
+// products, and the epilogue warps drain one of two accumulators while the other is filled.  Three
+// kernels differ in how a stage is filled:
 //   rows longer than 256 dimensions: TMA boxes of 128 vectors x 128 bytes, with the queries' beside;
 //   shorter ones: a tile is one contiguous piece of memory, so it comes as a single bulk copy, and
-//   two warps put it into the swizzled order.  TMA takes about 4 cycles a row of a box whatever
-//   its length (9 where rows are not a multiple of 64 bytes), which bound these tiles: 17.6 and 33 us
-//   for one query against 10^6 vectors of 128 and of 96 dimensions.  The queries' tile stays in
-//   shared memory while the vectors' tiles go by.
+//   two or four warps put it into the swizzled order, while the queries' tile stays in shared memory
+//   (one query and 10^6 vectors by boxes and by copies: 30.6 and 19.8 us at 96 dimensions, 29.5 and 17.4
+//   at 32, 41.7 and 33.7 at 224);
+//   many queries of long rows: pairs of CTAs, further down.
 //
 // The output is the larger part of the traffic for short rows.  Scores written straight from
 // registers are 128-byte pieces that straddle two lines when the row stride is odd (156 us against
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kMxThreads)
 constexpr int kMxBM = 128;         // vectors a tile
 constexpr int kMxMaxStages = 10;
 
-// What both kernels share: the epilogue's side.
+// What the kernels of one CTA share: the epilogue's side.
 template <int NT>
 struct MxEpi {
   static constexpr bool kStaged = NT >= 64;
@@ -269,7 +269,7 @@ template <int NT, int KB>
 struct MxCfg : MxEpi<NT> {
   static constexpr int kAtoms = KB / 64, kSfB = 512 * kAtoms;   // scale tiles a stage and side
   static constexpr int kStage = kMxBM * KB + NT * KB + 2 * kSfB;
-  static constexpr int kCtas = NT >= 128 ? 1 : KB == 64 ? (NT == 64 ? 2 : 4) : (NT == 64 ? 1 : 2);
+  static constexpr int kCtas = KB == 64 ? 4 : NT >= 64 ? 1 : 2;
   static constexpr int kBudget = (kCtas == 1 ? 226 : kCtas == 2 ? 112 : 55) * 1024 - 1024 - 512 -
                                  MxEpi<NT>::kOut;
   static constexpr int kStages = kBudget / kStage < kMxMaxStages ? kBudget / kStage : kMxMaxStages;
@@ -304,8 +304,8 @@ struct MxPackCfg : MxEpi<NT> {
 
 struct MxBars {
   uint64_t full[kMxMaxStages], empty[kMxMaxStages];   // the ring
-  uint64_t swz_full[3], swz_empty[3], q_full[2], q_empty[2];
-  uint64_t s_full[3], s_empty[3], drain;              // accumulators
+  uint64_t swz_full[2], swz_empty[2], q_full[2], q_empty[2];
+  uint64_t s_full[2], s_empty[2], drain;              // accumulators
   uint32_t tmem;
   int abort;
 };
@@ -1101,13 +1101,12 @@ cudaError_t mx_scores(const MxArgs& a) {
   CUtensorMap tmx, tmq;
   cudaError_t e;
   if (!mx_tmap(&tmq, a.qc, a.nb, a.m, KB, NT)) return cudaErrorInvalidValue;
-  // Bulk copies for rows shorter than a box.  Rows that fill one (128 and 256 dimensions) are moved
-  // by TMA at the rate of memory, and where the codes are most of the traffic the shorter way gains
-  // (one query and 10^6 vectors: 17.6 us against 21.9 at 128 dimensions, 29.4 against 35.2 at 256);
-  // where the output is, TMA is left to the stores (16 queries of 10^6 x 128: 33.2 us by boxes, 24.7;
-  // 1000 x 100003 x 256: 106, 92).
-  constexpr bool kBoxes = KB == 128 || NT < 128;    // (128 queries write more than they read there)
-  const bool full = 16 * a.nb == KB && 2 * a.m * (int64_t)sizeof(T) <= 17 * a.nb;
+  // Bulk copies for rows shorter than a box.  Rows that fill one come by boxes where that is faster: at
+  // 256 dimensions up to 64 queries (10^6 vectors, boxes and copies: one query 29.0 and 34.8 us, 16
+  // 35.6 and 35.9; 64 and 500000: 41.3 and 45.0; 1000 x 100003 fp32: 90.9 and 83.7), at 128 for one
+  // query (15.9 and 21.4 us; two queries 25.6 and 21.6).
+  constexpr bool kBoxes = KB == 128 || NT == 16;
+  const bool full = 16 * a.nb == KB && a.m <= (KB == 128 ? 64 : 1);
   if (!kBoxes || (16 * a.nb <= KB && !full)) {
     using C = MxPackCfg<NT, KB>;
     const int64_t steps = (vt + C::kSub - 1) / C::kSub;

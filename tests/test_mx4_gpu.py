@@ -116,7 +116,8 @@ def _check_scores(got, q, x, alpha, bias, d):
 @pytest.mark.parametrize("m,n,d", [(1, 1, 1), (1, 1000, 128), (3, 129, 100), (8, 257, 96), (16, 64, 33),
                                    (17, 300, 960), (33, 128, 256), (64, 500, 160), (65, 129, 129),
                                    (128, 640, 128), (129, 1000, 64), (200, 1, 320), (300, 777, 513),
-                                   (5, 20000, 40), (700, 1500, 1056), (260, 400, 4128)])
+                                   (5, 20000, 40), (700, 1500, 1056), (260, 400, 4128), (100, 200, 600),
+                                   (300, 100, 600), (2, 500, 128), (70, 300, 256), (64, 300, 256), (600, 300, 288)])
 def test_scores_match_the_oracle(m, n, d, out):
     import ivf_quantizer_b200 as q
     qs, x = _x(m, d, m + d).cuda(), _x(n, d, n + 1).cuda()
