@@ -34,6 +34,23 @@ def call(fn, name: str, device: torch.device, *args) -> None:
         check(code, name)
 
 
+_words: dict = {}   # the status word of each device: written only by a kernel that gave up
+
+
+def _word(device: torch.device):
+    """The device's status word; None while a graph is captured before there is one (its memory
+    and its zeroing would belong to the graph)."""
+    w = _words.get(device.index)
+    if w is None:
+        with torch.cuda.device(device):
+            if torch.cuda.is_current_stream_capturing():
+                return None
+            w = torch.zeros(1, dtype=torch.int32, device=device)
+            torch.cuda.current_stream().synchronize()   # zero before a kernel of any stream
+        _words[device.index] = w
+    return w
+
+
 def _rows(X: torch.Tensor, what: str):
     """(dtype code, rows, columns, row stride) of a 2-D tensor with contiguous rows."""
     if not (isinstance(X, torch.Tensor) and X.is_cuda and X.dim() == 2):
@@ -126,8 +143,25 @@ class MX4:
             q_scales = q_codes + split
             call(LIB.fgmm_mx4_encode, "fgmm_mx4_encode", dev, queries.data_ptr(), dt, M, D, ldq,
                  q_codes, q_scales)
-        out = empty(M, N, dtype, dev)
+        out, word = empty(M, N, dtype, dev), _word(dev)
         call(LIB.fgmm_mx4_scores, "fgmm_mx4_scores", dev, q_codes, q_scales, M, self.codes.data_ptr(),
              self.scales.data_ptr(), N, D, alpha, None if bias is None else bias.data_ptr(),
-             out.data_ptr(), out_dt, N, None)
+             out.data_ptr(), out_dt, N, None if word is None else word.data_ptr())
         return out
+
+    def status(self) -> int:
+        """Synchronise with the current stream and return (then clear) the status word that all
+        scores on this device share: ERR_TIMEOUT if a bounded wait expired, whose scores are then
+        undefined."""
+        dev = self.codes.device
+        word = _word(dev)
+        if word is None:
+            raise RuntimeError("the status cannot be read while a graph is captured")
+        with torch.cuda.device(dev):
+            code = int(word)
+            if code:
+                word.zero_()
+        return code
+
+    def check_status(self):
+        check(self.status(), "device status")

@@ -285,3 +285,17 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for g, w in zip(got, want):
         assert all(torch.equal(o, w) for o in g)
+
+
+def test_status_reports_and_clears_a_wait_that_gave_up():
+    import ivf_quantizer_b200 as q
+    from ivf_quantizer_b200 import _lib, mx4
+    index = q.MX4(_x(300, 64, 50).cuda())
+    index.scores(_x(3, 64, 51).cuda())
+    assert index.status() == _lib.OK
+    word = mx4._words[index.codes.device.index]     # the kernels' argument
+    word.fill_(_lib.ERR_TIMEOUT)
+    index.scores(_x(3, 64, 51).cuda())              # (a call that ends well leaves it)
+    with pytest.raises(_lib.FgmmError):
+        index.check_status()
+    assert index.status() == _lib.OK
