@@ -101,40 +101,58 @@ __device__ __forceinline__ int64_t mx_scale_at(int64_t row, int b, int nkc) {
   return ((row >> 7) * nkc + (b >> 2)) * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4 + (b & 3);
 }
 
+// 32 bytes (p aligned to them) that are not read again.
+__device__ __forceinline__ void mx_ld32(const void* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+
 // A thread encodes 32 bytes of a row at a time, four (fp32) or two (bf16) neighbouring lanes a block;
 // codes lie in the order of the threads, so a warp writes them as one contiguous piece.  Two pieces a
 // thread are loaded before either is used.  Bound by memory; a lane a 4 values took
-// 1266 us at 10^6 x 960 bf16 (issue), this takes 440.  VEC: rows allow 16-byte loads.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kMxThreads)
+// 1266 us at 10^6 x 960 bf16 (issue).  BYTES: what rows allow to load at once, 0 for single values.
+//
+// TILES: the rows are walked as if padded to whole scale tiles (4 blocks), so that four scales, the
+// padding included, leave as one word; lanes behind the last block idle.  10^6 rows, without and with,
+// us: fp32 x 128 100 and 91, x 448 350 and 325, x 960 762 and 665, bf16 x 512 225 and 213, x 960 443
+// and 423; but fp32 x 96 (a quarter idle) 80 and 89, bf16 x 160 91 and 113.  (32 bytes at once
+// against twice 16: 345 and 375 at fp32 x 512, no difference in bf16.)
+template <typename T, int BYTES, bool TILES>
+__global__ void __launch_bounds__(kMxThreads, TILES ? 6 : 1)
     mx4_encode_kernel(const T* __restrict__ X, int64_t n, int D, int64_t ldx, int nb, int nkc,
                       uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   using P = MxPiece<T>;
   constexpr int LB = 32 / P::N, U = 2;      // lanes a block, pieces in flight
   ptx::grid_release();                      // (kernels that read these codes may set themselves up)
-  MxPieces p(nb * LB);
+  MxPieces p((TILES ? 4 * nkc : nb) * LB);
   const int64_t rows = (n + 127) / 128 * 128;   // rows behind the last only have scales, 0
   // (whole warps stay together for the exchange: a warp leaves when its first piece is behind the end)
-  const int64_t pieces = rows * nb * LB;
+  const int64_t pieces = rows * p.segs;
   while (p.i - (threadIdx.x & 31) < pieces) {
     uint32_t w[U][8];
     int64_t at[U], row[U];
     int seg[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      at[u] = p.i, row[u] = p.row, seg[u] = p.seg;
+      at[u] = TILES ? p.row * (nb * LB) + p.seg : p.i;
+      row[u] = p.row, seg[u] = p.seg;
       p.next();
       const int d = seg[u] * P::N;
       const T* x = X + row[u] * ldx + d;
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[u][j] = 0u;
       if (row[u] < n) {
-        if (VEC && d + P::N <= D) {
-          const uint4 a = __ldcs(reinterpret_cast<const uint4*>(x));
-          const uint4 b = __ldcs(reinterpret_cast<const uint4*>(x) + 1);
-          w[u][0] = a.x, w[u][1] = a.y, w[u][2] = a.z, w[u][3] = a.w;
-          w[u][4] = b.x, w[u][5] = b.y, w[u][6] = b.z, w[u][7] = b.w;
-        } else {
+        if (BYTES > 0 && d + P::N <= D) {
+          if constexpr (BYTES == 32) {
+            mx_ld32(x, w[u]);
+          } else {
+            const uint4 a = __ldcs(reinterpret_cast<const uint4*>(x));
+            const uint4 b = __ldcs(reinterpret_cast<const uint4*>(x) + 1);
+            w[u][0] = a.x, w[u][1] = a.y, w[u][2] = a.z, w[u][3] = a.w;
+            w[u][4] = b.x, w[u][5] = b.y, w[u][6] = b.z, w[u][7] = b.w;
+          }
+        } else if (!TILES || d < D) {
 #pragma unroll
           for (int j = 0; j < P::N; ++j)
             if (d + j < D) P::put(w[u], j, mx_ld(x + j));
@@ -158,10 +176,18 @@ __global__ void __launch_bounds__(kMxThreads)
                                           P::at(w[u], j + 2) * inv, P::at(w[u], j + 3) * inv)
              << (4 * j);
       if (bad) c = 0;
-      if (at[u] >= pieces) continue;
-      if (row[u] < n) reinterpret_cast<typename P::Codes*>(codes)[at[u]] = c;
+      uint32_t four = s;                    // TILES: the scales of four blocks, in the lanes of the first
+      if constexpr (TILES) {
+        four |= __shfl_xor_sync(0xffffffffu, four, LB) << 8;
+        four |= __shfl_xor_sync(0xffffffffu, four, 2 * LB) << 16;
+      }
+      if (row[u] >= rows) continue;
+      if (row[u] < n && (!TILES || seg[u] < nb * LB)) reinterpret_cast<typename P::Codes*>(codes)[at[u]] = c;
       const int b = seg[u] / LB;
-      if (seg[u] % LB == 0) {
+      if constexpr (TILES) {
+        if (seg[u] % (4 * LB) == 0)
+          *reinterpret_cast<uint32_t*>(scales + mx_scale_at(row[u], b, nkc)) = four;
+      } else if (seg[u] % LB == 0) {
         scales[mx_scale_at(row[u], b, nkc)] = row[u] < n ? (uint8_t)s : 0;
         if (b == nb - 1)                    // and the padding of the last scale tile
           for (int z = nb; z < 4 * nkc; ++z) scales[mx_scale_at(row[u], z, nkc)] = 0;
@@ -1158,14 +1184,26 @@ cudaError_t mx_scores_kb(const MxArgs& a) {
   return a.nb <= 4 ? mx_scores_nt<64, T>(a) : mx_scores_nt<128, T>(a);
 }
 
-// Blocks for `pieces` threads' worth of work: enough to fill the device, fewer when there is less.
-cudaError_t mx_blocks(int64_t pieces, unsigned* grid) {
+template <typename T>
+cudaError_t mx_encode(const T* X, int64_t n, int D, int64_t ldx, int nb, int nkc, uint8_t* codes,
+                      uint8_t* scales, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int64_t need = (pieces + kMxThreads - 1) / kMxThreads, most = (int64_t)sms * 16;
-  *grid = (unsigned)(need < most ? need : most);
-  return e;
+  if (e != cudaSuccess) return e;
+  const auto rows_at = [&](int b) { return (uintptr_t)X % b == 0 && ldx * sizeof(T) % b == 0; };
+  const int pad = 4 * nkc - nb;
+  const bool tiles = pad <= nkc / 2 && rows_at(16);   // at most an eighth of the lanes idle
+  // fill the device; fewer blocks when there is less, and two pieces a thread once that fills it too
+  int64_t blocks = (n + 127) / 128 * 128 * (tiles ? 4 * nkc : nb) * sizeof(T);
+  blocks = (blocks + kMxThreads - 1) / kMxThreads;
+  if (tiles && blocks > 12 * sms) blocks = (blocks + 1) / 2;
+  const int64_t most = (int64_t)sms * (tiles ? 32 : 16);
+  const unsigned grid = (unsigned)(blocks < most ? blocks : most);
+  auto* k = tiles ? (rows_at(32) ? mx4_encode_kernel<T, 32, true> : mx4_encode_kernel<T, 16, true>)
+                  : (rows_at(16) ? mx4_encode_kernel<T, 16, false> : mx4_encode_kernel<T, 0, false>);
+  k<<<grid, kMxThreads, 0, s>>>(X, n, D, ldx, nb, nkc, codes, scales);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -1174,20 +1212,9 @@ cudaError_t mx_blocks(int64_t pieces, unsigned* grid) {
 cudaError_t launch_mx4_encode(const void* X, int x_dtype, int64_t n, int D, int64_t ldx,
                               uint8_t* codes, uint8_t* scales, cudaStream_t s) {
   const int nb = (D + 31) / 32, nkc = (nb + 3) / 4;
-  const int eb = x_dtype == FGMM_F32 ? 4 : 2;
-  const bool vec = (uintptr_t)X % 16 == 0 && ldx * eb % 16 == 0;
-  unsigned grid = 0;
-  cudaError_t e = mx_blocks((n + 127) / 128 * 128 * nb * eb, &grid);
-  if (e != cudaSuccess) return e;
-  if (x_dtype == FGMM_F32) {
-    auto* k = vec ? mx4_encode_kernel<float, true> : mx4_encode_kernel<float, false>;
-    k<<<grid, kMxThreads, 0, s>>>(static_cast<const float*>(X), n, D, ldx, nb, nkc, codes, scales);
-  } else {
-    auto* k = vec ? mx4_encode_kernel<__nv_bfloat16, true> : mx4_encode_kernel<__nv_bfloat16, false>;
-    k<<<grid, kMxThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(X), n, D, ldx, nb, nkc, codes,
-                                  scales);
-  }
-  return cudaGetLastError();
+  if (x_dtype == FGMM_F32)
+    return mx_encode(static_cast<const float*>(X), n, D, ldx, nb, nkc, codes, scales, s);
+  return mx_encode(static_cast<const __nv_bfloat16*>(X), n, D, ldx, nb, nkc, codes, scales, s);
 }
 
 cudaError_t launch_mx4_decode(const uint8_t* codes, const uint8_t* scales, int64_t n, int D,

@@ -299,3 +299,35 @@ def test_status_reports_and_clears_a_wait_that_gave_up():
     with pytest.raises(_lib.FgmmError):
         index.check_status()
     assert index.status() == _lib.OK
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n", [1, 130, 257])
+@pytest.mark.parametrize("d", [97, 104, 112, 220, 224, 352, 448, 480, 512])
+def test_encode_rows_that_fill_their_scale_tiles(d, n, dtype):
+    """Rows whose blocks fill at least 7/8 of their scale tiles, and ones that just do not, at each
+    alignment of the rows."""
+    import ivf_quantizer_b200 as q
+    wide = _x(n, 544, n + d, dtype).cuda()
+    for x in (wide[:, :d].contiguous(), wide[:, :d], wide[:, 8:d + 8], wide[:, 4:d + 4], wide[:, 1:d + 1]):
+        _same_codes(q.MX4(x), x)
+
+
+@pytest.mark.parametrize("n,d,dtype", [(400001, 128, torch.float32), (120001, 960, torch.bfloat16),
+                                       (700001, 96, torch.float32)])
+def test_encode_many_rows(n, d, dtype):
+    """More pieces than threads: rows encoded alone have the same codes and scales."""
+    import ivf_quantizer_b200 as q
+    x = _x(n, d, 60, dtype).cuda()
+    m = q.MX4(x)
+    nkc = -(-d // 128)
+    for r in (0, 128 * 700, n // 128 * 128 - 12800, n // 128 * 128):
+        part = x[r:r + 12800]
+        p = q.MX4(part)
+        assert torch.equal(m.codes[r:r + 12800], p.codes)
+        t = r // 128 * nkc * 512
+        assert torch.equal(m.scales[t:t + p.scales.numel()], p.scales)
+    _same_codes(p, part)
+    out = m.decode()
+    s = torch.randint(0, n, (300,), generator=torch.Generator().manual_seed(61)).cuda()
+    np.testing.assert_array_equal(_np(out[s]), M.decode(*M.encode(_np(x[s])), d))
