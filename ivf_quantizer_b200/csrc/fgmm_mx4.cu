@@ -108,10 +108,17 @@ __device__ __forceinline__ void mx_ld32(const void* p, uint32_t (&w)[8]) {
                : "l"(p));
 }
 
+__device__ __forceinline__ void mx_st32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // A thread encodes 32 bytes of a row at a time, four (fp32) or two (bf16) neighbouring lanes a block;
 // codes lie in the order of the threads, so a warp writes them as one contiguous piece.  Two pieces a
 // thread are loaded before either is used.  Bound by memory; a lane a 4 values took
-// 1266 us at 10^6 x 960 bf16 (issue).  BYTES: what rows allow to load at once, 0 for single values.
+// 1266 us at 10^6 x 960 bf16 (issue).  BYTES: what rows allow to load at once
+// (bf16 x 960 by 8 and 4 bytes, row strides 964 and 962, 469 and 523 us; by single values both 890).
 //
 // TILES: the rows are walked as if padded to whole scale tiles (4 blocks), so that four scales, the
 // padding included, leave as one word; lanes behind the last block idle.  10^6 rows, without and with,
@@ -143,9 +150,19 @@ __global__ void __launch_bounds__(kMxThreads, TILES ? 6 : 1)
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[u][j] = 0u;
       if (row[u] < n) {
-        if (BYTES > 0 && d + P::N <= D) {
+        if (BYTES > (int)sizeof(T) && d + P::N <= D) {
           if constexpr (BYTES == 32) {
             mx_ld32(x, w[u]);
+          } else if constexpr (BYTES < 16) {        // (cached: the same lines are read several times)
+#pragma unroll
+            for (int j = 0; j < 8; j += BYTES / 4) {
+              if constexpr (BYTES == 8) {
+                const uint2 a = __ldg(reinterpret_cast<const uint2*>(x) + j / 2);
+                w[u][j] = a.x, w[u][j + 1] = a.y;
+              } else {
+                w[u][j] = __ldg(reinterpret_cast<const uint32_t*>(x) + j);
+              }
+            }
           } else {
             const uint4 a = __ldcs(reinterpret_cast<const uint4*>(x));
             const uint4 b = __ldcs(reinterpret_cast<const uint4*>(x) + 1);
@@ -196,35 +213,36 @@ __global__ void __launch_bounds__(kMxThreads, TILES ? 6 : 1)
   }
 }
 
-// One warp decodes 512 bytes of output (128 fp32 or 256 bf16 dimensions) of the rows r, r + 32,
-// r + 64, r + 96 of a 128-row tile: 16 bytes a lane and row, and the four rows' scales of a block lie
-// in the same 16 bytes of the scale tile.  Bound by writing; with the encoder's mapping (a flat
-// sequence of pieces) the address arithmetic of every 16 bytes took it to 979 us at 10^6 x 960 fp32,
-// against 685.
-template <typename T, bool VEC>
+// A thread decodes BYTES of the rows r, r + 32, r + 64, r + 96 of a 128-row tile: the four rows' scales
+// of a block lie in the same 16 bytes of the scale tile.  Threads follow one another along a row, then
+// to the next one.  Bound by writing.  AT: the bytes that rows allow to store at once.  10^6 rows, us,
+// with a warp on 512 bytes of a row, 16 a lane, and so: fp32 x 960 671 and 645, bf16 x 960 447 and 366,
+// bf16 x 128 111 and 51.  With the encoder's mapping (a sequence of pieces of consecutive rows) the
+// address arithmetic took it to 979 at fp32 x 960.  Rows off a 16-byte boundary by single values, with
+// 8 a thread, and so: bf16 x 960 with a row stride of 964 2714 and 510, of 962 522, of 961 1040.
+template <typename T, int BYTES, int AT>
 __global__ void __launch_bounds__(kMxThreads)
     mx4_decode_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                      int64_t n, int D, int nb, int nkc, int nkg, int64_t groups, T* __restrict__ out,
+                      int64_t n, int D, int nb, int nkc, int segs, int64_t pieces, T* __restrict__ out,
                       int64_t ldo) {
-  constexpr int N = 16 / sizeof(T);
-  using Codes = std::conditional_t<N == 4, uint16_t, uint32_t>;
+  constexpr int N = BYTES / sizeof(T), WORDS = BYTES / 4;
+  using Codes = std::conditional_t<N == 4, uint16_t, std::conditional_t<N == 8, uint32_t, uint64_t>>;
   ptx::grid_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t step = (int64_t)gridDim.x * (kMxThreads / 32);
-  for (int64_t g = (int64_t)blockIdx.x * (kMxThreads / 32) + (threadIdx.x >> 5); g < groups; g += step) {
-    const int64_t rr = g / nkg;                     // row tile * 32 + row within the quarter
-    const int kg = (int)(g - rr * nkg), d = (kg * 32 + lane) * N;
-    if (d >= D) continue;
+  const int64_t step = (int64_t)gridDim.x * kMxThreads;
+  for (int64_t i0 = (int64_t)blockIdx.x * kMxThreads; i0 + threadIdx.x < pieces; i0 += step) {
+    const int64_t r0 = i0 / segs;                   // (the block's; the thread's from it by 32 bits)
+    const uint32_t at = (uint32_t)(i0 - r0 * segs) + threadIdx.x, dr = at / (uint32_t)segs;
+    const int64_t rr = r0 + dr;                     // row tile * 32 + row within the quarter
+    const int d = (int)(at - dr * segs) * N;
     const int64_t row0 = (rr >> 5) * 128 + (rr & 31);
     const uint4 sw = __ldg(reinterpret_cast<const uint4*>(
         scales + ((rr >> 5) * nkc + (d >> 7)) * 512 + (rr & 31) * 16));
     const uint32_t words[4] = {sw.x, sw.y, sw.z, sw.w};
     const uint8_t* from = codes + row0 * nb * 16 + (d >> 1);
-    uint32_t c[4];
+    Codes c[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      c[q] = row0 + 32 * q < n
-                 ? (uint32_t)__ldcs(reinterpret_cast<const Codes*>(from + (int64_t)32 * q * nb * 16)) : 0u;
+      c[q] = row0 + 32 * q < n ? __ldcs(reinterpret_cast<const Codes*>(from + (int64_t)32 * q * nb * 16)) : Codes(0);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       if (row0 + 32 * q >= n) break;
@@ -232,22 +250,29 @@ __global__ void __launch_bounds__(kMxThreads)
       T* o = out + (row0 + 32 * q) * ldo + d;
       float v[N];
 #pragma unroll
-      for (int j = 0; j < N; ++j) v[j] = mx_value(c[q] >> (4 * j)) * s;
-      if (VEC && d + N <= D) {
-        uint4 w;
-        if constexpr (N == 4) {
-          w = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                         __float_as_uint(v[3]));
-        } else {
-          uint32_t h[4];                            // (exact: a code has two significant bits)
+      for (int j = 0; j < N; ++j) v[j] = mx_value((uint32_t)(c[q] >> (4 * j))) * s;
+      if (AT >= 4 && d + N <= D) {
+        uint32_t w[WORDS];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < WORDS; ++j) {
+          if constexpr (sizeof(T) == 4) {
+            w[j] = __float_as_uint(v[j]);
+          } else {                                  // (exact: a code has two significant bits)
             const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-            h[j] = reinterpret_cast<const uint32_t&>(t);
+            w[j] = reinterpret_cast<const uint32_t&>(t);
           }
-          w = make_uint4(h[0], h[1], h[2], h[3]);
         }
-        __stcs(reinterpret_cast<uint4*>(o), w);
+        if constexpr (AT == 32) {
+          mx_st32(o, w);
+        } else {
+#pragma unroll
+          for (int j = 0; j < WORDS; j += AT / 4) {
+            uint32_t* to = reinterpret_cast<uint32_t*>(o) + j;
+            if constexpr (AT == 16) __stcs(reinterpret_cast<uint4*>(to), make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]));
+            else if constexpr (AT == 8) __stcs(reinterpret_cast<uint2*>(to), make_uint2(w[j], w[j + 1]));
+            else __stcs(to, w[j]);
+          }
+        }
       } else {
 #pragma unroll
         for (int j = 0; j < N; ++j)
@@ -1201,9 +1226,32 @@ cudaError_t mx_encode(const T* X, int64_t n, int D, int64_t ldx, int nb, int nkc
   const int64_t most = (int64_t)sms * (tiles ? 32 : 16);
   const unsigned grid = (unsigned)(blocks < most ? blocks : most);
   auto* k = tiles ? (rows_at(32) ? mx4_encode_kernel<T, 32, true> : mx4_encode_kernel<T, 16, true>)
-                  : (rows_at(16) ? mx4_encode_kernel<T, 16, false> : mx4_encode_kernel<T, 0, false>);
+            : rows_at(16)                  ? mx4_encode_kernel<T, 16, false>
+            : rows_at(8)                   ? mx4_encode_kernel<T, 8, false>
+            : sizeof(T) == 4 || rows_at(4) ? mx4_encode_kernel<T, 4, false>
+                                           : mx4_encode_kernel<T, 2, false>;
   k<<<grid, kMxThreads, 0, s>>>(X, n, D, ldx, nb, nkc, codes, scales);
   return cudaGetLastError();
+}
+
+template <typename T, int BYTES, int AT>
+cudaError_t mx_decode_by(const uint8_t* codes, const uint8_t* scales, int64_t n, int D, T* out,
+                         int64_t ldo, cudaStream_t s) {
+  constexpr int N = BYTES / sizeof(T);
+  const int nb = (D + 31) / 32, nkc = (nb + 3) / 4, segs = (D + N - 1) / N;
+  const int64_t pieces = (n + 127) / 128 * 32 * segs, blocks = (pieces + kMxThreads - 1) / kMxThreads;
+  return mx_launch(mx4_decode_kernel<T, BYTES, AT>, (unsigned)(blocks < (1 << 30) ? blocks : (1 << 30)),
+                   kMxThreads, 0, s, codes, scales, n, D, nb, nkc, segs, pieces, out, ldo);
+}
+template <typename T>
+cudaError_t mx_decode(const uint8_t* codes, const uint8_t* scales, int64_t n, int D, T* out, int64_t ldo,
+                      cudaStream_t s) {
+  const auto rows_at = [&](int b) { return (uintptr_t)out % b == 0 && ldo * sizeof(T) % b == 0; };
+  if (rows_at(32)) return mx_decode_by<T, 32, 32>(codes, scales, n, D, out, ldo, s);
+  if (rows_at(16)) return mx_decode_by<T, 16, 16>(codes, scales, n, D, out, ldo, s);
+  if (rows_at(8)) return mx_decode_by<T, 16, 8>(codes, scales, n, D, out, ldo, s);
+  if (sizeof(T) == 4 || rows_at(4)) return mx_decode_by<T, 16, 4>(codes, scales, n, D, out, ldo, s);
+  return mx_decode_by<T, 8, 2>(codes, scales, n, D, out, ldo, s);
 }
 
 }  // namespace
@@ -1219,20 +1267,8 @@ cudaError_t launch_mx4_encode(const void* X, int x_dtype, int64_t n, int D, int6
 
 cudaError_t launch_mx4_decode(const uint8_t* codes, const uint8_t* scales, int64_t n, int D,
                               void* out, int out_dtype, int64_t ldo, cudaStream_t s) {
-  const int nb = (D + 31) / 32, nkc = (nb + 3) / 4;
-  const int eb = out_dtype == FGMM_F32 ? 4 : 2;
-  const bool vec = (uintptr_t)out % 16 == 0 && ldo * eb % 16 == 0;
-  const int nkg = (D * eb + 511) / 512;             // 512-byte pieces of a row
-  const int64_t groups = (n + 127) / 128 * 32 * nkg, blocks = (groups + kMxThreads / 32 - 1) / (kMxThreads / 32);
-  const unsigned grid = (unsigned)(blocks < (1 << 30) ? blocks : (1 << 30));
-  if (out_dtype == FGMM_F32) {
-    auto* k = vec ? mx4_decode_kernel<float, true> : mx4_decode_kernel<float, false>;
-    return mx_launch(k, grid, kMxThreads, 0, s, codes, scales, n, D, nb, nkc, nkg, groups,
-                     static_cast<float*>(out), ldo);
-  }
-  auto* k = vec ? mx4_decode_kernel<__nv_bfloat16, true> : mx4_decode_kernel<__nv_bfloat16, false>;
-  return mx_launch(k, grid, kMxThreads, 0, s, codes, scales, n, D, nb, nkc, nkg, groups,
-                   static_cast<__nv_bfloat16*>(out), ldo);
+  if (out_dtype == FGMM_F32) return mx_decode(codes, scales, n, D, static_cast<float*>(out), ldo, s);
+  return mx_decode(codes, scales, n, D, static_cast<__nv_bfloat16*>(out), ldo, s);
 }
 
 cudaError_t launch_mx4_scores(const uint8_t* q_codes, const uint8_t* q_scales, int64_t m,

@@ -331,3 +331,33 @@ def test_encode_many_rows(n, d, dtype):
     out = m.decode()
     s = torch.randint(0, n, (300,), generator=torch.Generator().manual_seed(61)).cuda()
     np.testing.assert_array_equal(_np(out[s]), M.decode(*M.encode(_np(x[s])), d))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,d", [(1, 3), (130, 97), (31, 100), (257, 128), (65, 530)])
+def test_decode_into_rows_of_each_alignment(n, d, dtype):
+    """Rows of a larger buffer at offsets and strides of 32, 16, 8 and 4 bytes and of one value; what
+    lies beside them stays."""
+    import ivf_quantizer_b200 as q
+    from ivf_quantizer_b200 import _lib
+    m = q.MX4(_x(n, d, 70 + d).cuda())
+    want = m.decode(dtype)
+    np.testing.assert_array_equal(_np(want), M.decode(*M.encode(_np(_x(n, d, 70 + d))), d))
+    stream = torch.cuda.current_stream().cuda_stream
+    code = _lib.F32 if dtype == torch.float32 else _lib.BF16
+    for off, ld in ((0, 544), (16, 560), (8, 552), (4, 548), (2, 546), (1, 545), (0, 545), (1, 544)):
+        out = torch.full((n + 1, ld), 7.0, device="cuda", dtype=dtype)
+        assert _lib.LIB.fgmm_mx4_decode(m.codes.data_ptr(), m.scales.data_ptr(), n, d,
+                                        out[:, off:].data_ptr(), code, ld, stream) == _lib.OK
+        assert torch.equal(out[:n, off:off + d], want)
+        out[:n, off:off + d] = 7.0
+        assert (out == 7).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_encode_rows_of_each_alignment(dtype):
+    import ivf_quantizer_b200 as q
+    for off, ld in ((0, 544), (16, 560), (8, 552), (4, 548), (2, 546), (1, 545), (0, 545), (1, 544)):
+        wide = _x(130, ld, 80 + off, dtype).cuda()
+        for d in (97, 100, 160, 520):
+            _same_codes(q.MX4(wide[:, off:off + d]), wide[:, off:off + d])
