@@ -122,7 +122,7 @@ __device__ __forceinline__ void mx_st32(void* p, const uint32_t (&w)[8]) {
 //
 // TILES: the rows are walked as if padded to whole scale tiles (4 blocks), so that four scales, the
 // padding included, leave as one word; lanes behind the last block idle.  10^6 rows, without and with,
-// us: fp32 x 128 100 and 91, x 448 350 and 325, x 960 762 and 665, bf16 x 512 225 and 213, x 960 443
+// us: fp32 x 128 100 and 91, x 448 350 and 325, x 960 762 and 690, bf16 x 512 225 and 213, x 960 443
 // and 423; but fp32 x 96 (a quarter idle) 80 and 89, bf16 x 160 91 and 113.  (32 bytes at once
 // against twice 16: 345 and 375 at fp32 x 512, no difference in bf16.)
 template <typename T, int BYTES, bool TILES>
