@@ -581,6 +581,7 @@ __global__ void __launch_bounds__(MxEpi<NT>::kThreads, MxCfg<NT, KB>::kCtas)
           ok = false;
           break;
         }
+        ptx::tc_fence_after();  // the epilogue's reads of the buffer come before these products
         const uint32_t d_tmem = tmem + buf * NT;
         for (int k = 0; k < nst; ++k, ++it) {
           if (!ptx::mbar_wait_all(&bars->full[s], ph, abort)) {
@@ -738,6 +739,7 @@ __global__ void __launch_bounds__(MxPackCfg<NT, KB>::kThreads, MxPackCfg<NT, KB>
         // (the scale columns of the buffer's last step are free with its sums)
         if (j >= C::kBufs && !ptx::mbar_wait_all(&bars->s_empty[buf], use ^ 1, abort)) ok = false;
         if (!ok) break;
+        ptx::tc_fence_after();  // the epilogue's reads of the buffer come before these products
         if (w.q() != qt) {
           qt = w.q();
           ok = ptx::mbar_wait_all(&bars->q_full[jq & 1], (jq >> 1) & 1, abort);
@@ -958,6 +960,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxPairCfg<T>::kThrea
         if (j >= 2) ok = ptx::mbar_wait_cluster_all(&bars->s_empty[buf], ((j >> 1) - 1) & 1, abort);
         if (ok && j >= 1) ok = ptx::mbar_wait_cluster_all(&bars->overlap, (j - 1) & 1, abort);
         if (!ok) break;
+        ptx::tc_fence_after();  // both epilogues' reads of these columns come before the products
         const uint32_t d_tmem = tmem + (buf ? C::kAcc1 : 0);
         for (int k = 0; k < nst; ++k) {
           ok = ptx::mbar_wait_cluster_all(&bars->full[s], ph, abort);
