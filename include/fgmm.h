@@ -445,7 +445,11 @@ int fgmm_ivf_search(int K, int D, const float* centroids, const int64_t* offsets
  * ranks by L2 distance).  Products are exact, sums are fp32 (what is below 2^-126 may come out as
  * 0, what is above the largest fp32 as infinity); out_dtype FGMM_F32 or FGMM_BF16, rows of stride
  * ldo >= N.  status: optional device int, set to FGMM_ERR_TIMEOUT if a bounded wait of the
- * kernel expires (the output is then undefined), else left as it is. */
+ * kernel expires (the output is then undefined), else left as it is.
+ *
+ * fgmm_mx4_status_word: a word for that argument which the library holds on the current device, one
+ * for all calls: 0 at the start, never freed, so calls on every stream and in every captured
+ * graph may share it.  Whoever reads it clears it. */
 #define FGMM_MX4_MAX_ROWS ((1ll << 31) - 1024)
 #define FGMM_MX4_MAX_D (1 << 20)
 size_t fgmm_mx4_codes_bytes(int64_t N, int D);
@@ -458,6 +462,7 @@ int fgmm_mx4_scores(const uint8_t* q_codes, const uint8_t* q_scales, int64_t M,
                     const uint8_t* codes, const uint8_t* scales, int64_t N, int D, float alpha,
                     const float* bias, void* out, int out_dtype, int64_t ldo, int* status,
                     fgmm_stream_t stream);
+int fgmm_mx4_status_word(int** word);
 
 /* One draw per row of scores from its truncated softmax, with given uniforms (the method's
  * randomness is an input, as in fgmm_kmeans_seed).  Stateless, device pointers, asynchronous.

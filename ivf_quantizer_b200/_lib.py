@@ -93,6 +93,7 @@ SIGNATURES = {
     "fgmm_mx4_decode": (_int, [_vp, _vp, _i64, _int, _vp, _int, _i64, _vp]),
     "fgmm_mx4_scores": (_int, [_vp, _vp, _i64, _vp, _vp, _i64, _int, _flt, _vp, _vp, _int, _i64,
                                _vp, _vp]),
+    "fgmm_mx4_status_word": (_int, [_vp]),
     "fgmm_sample_logits": (_int, [_vp, _int, _i64, _int, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                   _vp]),
     "fgmm_em_step_host": (_int, [_vp, _vp, _int, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),

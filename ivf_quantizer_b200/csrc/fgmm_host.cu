@@ -1098,6 +1098,11 @@ int fgmm_mx4_scores(const uint8_t* q_codes, const uint8_t* q_scales, int64_t M,
                                     out_dtype, ldo, status, (cudaStream_t)stream));
 }
 
+int fgmm_mx4_status_word(int** word) {
+  if (!word) return FGMM_ERR_INVALID_ARG;
+  return map_cuda(mx4_status_word(word));
+}
+
 int fgmm_sample_logits(const void* logits, int dtype, int64_t rows, int V, int64_t ld,
                        const float* temperature, const int32_t* top_k, const float* top_p,
                        const float* min_p, const double* u, int32_t* ids, float* prob,

@@ -272,6 +272,7 @@ cudaError_t launch_mx4_scores(const uint8_t* q_codes, const uint8_t* q_scales, i
                               const uint8_t* codes, const uint8_t* scales, int64_t n, int D,
                               float alpha, const float* bias, void* out, int out_dtype,
                               int64_t ldo, int* status, cudaStream_t s);
+cudaError_t mx4_status_word(int** word);
 // draws from truncated softmaxes (fgmm_sample.cu)
 cudaError_t launch_sample_logits(const void* logits, int dtype, int64_t rows, int V, int64_t ld,
                                  const float* temperature, const int32_t* top_k,

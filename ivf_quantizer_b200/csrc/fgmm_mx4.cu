@@ -15,6 +15,10 @@
 namespace fgmm {
 namespace {
 
+// The word that fgmm_mx4_status_word gives out.  A variable of the module: there before the first
+// call, whatever captures or allocates at that time, and the same for every thread.
+__device__ int mx_status_word = FGMM_OK;
+
 constexpr int kMxThreads = 256;
 
 __device__ __forceinline__ float mx_ld(const float* p) { return __ldg(p); }
@@ -1281,6 +1285,10 @@ cudaError_t launch_mx4_scores(const uint8_t* q_codes, const uint8_t* q_scales, i
   const MxArgs a = {q_codes, q_scales, codes, scales, m, n, (D + 31) / 32, alpha, bias, out, ldo,
                     status, s};
   return out_dtype == FGMM_F32 ? mx_scores_kb<float>(a) : mx_scores_kb<__nv_bfloat16>(a);
+}
+
+cudaError_t mx4_status_word(int** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), mx_status_word);
 }
 
 }  // namespace fgmm

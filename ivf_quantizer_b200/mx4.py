@@ -4,6 +4,8 @@ fgmm_mx4_encode / fgmm_mx4_decode / fgmm_mx4_scores (include/fgmm.h).  CUDA tens
 argument marshalling only.  Work runs on the current stream of the tensors' device."""
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import _lib
@@ -34,21 +36,29 @@ def call(fn, name: str, device: torch.device, *args) -> None:
         check(code, name)
 
 
-_words: dict = {}   # the status word of each device: written only by a kernel that gave up
+_words: dict = {}   # the library's status word of each device: written only by a kernel that gave up
 
 
-def _word(device: torch.device):
-    """The device's status word; None while a graph is captured before there is one (its memory
-    and its zeroing would belong to the graph)."""
+def _word(device: torch.device) -> torch.Tensor:
+    """The device's status word.  Memory of the library, so that it does not matter what the first
+    call is part of: a captured graph, another thread's first call, inference mode."""
     w = _words.get(device.index)
     if w is None:
+        at = ctypes.c_void_p()
         with torch.cuda.device(device):
-            if torch.cuda.is_current_stream_capturing():
-                return None
-            w = torch.zeros(1, dtype=torch.int32, device=device)
-            torch.cuda.current_stream().synchronize()   # zero before a kernel of any stream
+            check(LIB.fgmm_mx4_status_word(ctypes.byref(at)), "fgmm_mx4_status_word")
+        with torch.inference_mode(False):
+            w = torch.as_tensor(_Int32(at.value), device=device)
         _words[device.index] = w
     return w
+
+
+class _Int32:
+    """One int32 at a device address, for torch.as_tensor."""
+
+    def __init__(self, at: int):
+        self.__cuda_array_interface__ = {"shape": (1,), "typestr": "<i4", "data": (at, False),
+                                         "version": 3}
 
 
 def _rows(X: torch.Tensor, what: str):
@@ -146,7 +156,7 @@ class MX4:
         out, word = empty(M, N, dtype, dev), _word(dev)
         call(LIB.fgmm_mx4_scores, "fgmm_mx4_scores", dev, q_codes, q_scales, M, self.codes.data_ptr(),
              self.scales.data_ptr(), N, D, alpha, None if bias is None else bias.data_ptr(),
-             out.data_ptr(), out_dt, N, None if word is None else word.data_ptr())
+             out.data_ptr(), out_dt, N, word.data_ptr())
         return out
 
     def status(self) -> int:
@@ -155,9 +165,9 @@ class MX4:
         undefined."""
         dev = self.codes.device
         word = _word(dev)
-        if word is None:
-            raise RuntimeError("the status cannot be read while a graph is captured")
         with torch.cuda.device(dev):
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("the status cannot be read while a graph is captured")
             code = int(word)
             if code:
                 word.zero_()
