@@ -5,6 +5,7 @@ argument marshalling only.  Work runs on the current stream of the tensors' devi
 from __future__ import annotations
 
 import ctypes
+import threading
 
 import torch
 
@@ -37,6 +38,8 @@ def call(fn, name: str, device: torch.device, *args) -> None:
 
 
 _words: dict = {}   # the library's status word of each device: written only by a kernel that gave up
+_reports: dict = {}   # how often each device's word has been found set, and cleared
+_reports_lock = threading.Lock()
 
 
 def _word(device: torch.device) -> torch.Tensor:
@@ -86,7 +89,7 @@ class MX4:
     def __init__(self, X: torch.Tensor):
         dt, N, D, ldx = _rows(X, "X")
         dev, nb = X.device, -(-D // _lib.MX4_BLOCK)
-        self.shape = (N, D)
+        self.shape, self._reports = (N, D), _reports.get(dev.index, 0)
         self.codes = empty(N, nb * 16, torch.uint8, dev)
         self.scales = empty(-(-N // 128) * -(-nb // 4) * 512, None, torch.uint8, dev)
         call(LIB.fgmm_mx4_encode, "fgmm_mx4_encode", dev, X.data_ptr(), dt, N, D, ldx,
@@ -104,6 +107,7 @@ class MX4:
             raise ValueError("codes or scales have the wrong size for this D")
         self = cls.__new__(cls)
         self.shape, self.codes, self.scales = (N, D), codes, scales
+        self._reports = _reports.get(codes.device.index, 0)
         return self
 
     @property
@@ -160,17 +164,23 @@ class MX4:
         return out
 
     def status(self) -> int:
-        """Synchronise with the current stream and return (then clear) the status word that all
-        scores on this device share: ERR_TIMEOUT if a bounded wait expired, whose scores are then
-        undefined."""
+        """Synchronise with the current stream and return ERR_TIMEOUT if, since the last call on this
+        MX4 (or since it was made), a bounded wait of any scores on its device expired; such scores
+        are undefined.  The device has one status word: what one MX4 reads and clears, the others
+        are told at their next call."""
         dev = self.codes.device
         word = _word(dev)
-        with torch.cuda.device(dev):
+        with _reports_lock, torch.cuda.device(dev):
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("the status cannot be read while a graph is captured")
-            code = int(word)
-            if code:
+            if int(word):
                 word.zero_()
+                torch.cuda.current_stream().synchronize()
+                # counted after clearing: it covers what a kernel noted in between
+                _reports[dev.index] = _reports.get(dev.index, 0) + 1
+            reports = _reports.get(dev.index, 0)
+            code = _lib.OK if reports == self._reports else _lib.ERR_TIMEOUT
+            self._reports = reports
         return code
 
     def check_status(self):

@@ -110,3 +110,46 @@ def test_everything_captured_in_a_fresh_process():
     r = subprocess.run([sys.executable, "-c", textwrap.dedent(code)], capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.gpu
+def test_a_report_reaches_every_index_of_the_device():
+    from ivf_quantizer_b200 import _lib, mx4
+    a, b, queries = _index(300, 64, 7), _index(200, 64, 8), _index(3, 64, 9)
+    a.scores(queries), b.scores(queries)
+    assert a.status() == b.status() == _lib.OK
+    word = mx4._words[a.codes.device.index]
+    word.fill_(_lib.ERR_TIMEOUT)
+    c = _index(100, 64, 10)                             # made before anyone has read it
+    assert a.status() == _lib.ERR_TIMEOUT
+    d = _index(100, 64, 11)                             # and after
+    assert a.status() == _lib.OK and d.status() == _lib.OK
+    assert b.status() == _lib.ERR_TIMEOUT and c.status() == _lib.ERR_TIMEOUT
+    assert b.status() == _lib.OK and c.status() == _lib.OK and int(word) == 0
+
+
+@pytest.mark.gpu
+def test_a_report_noted_while_the_word_is_cleared_is_not_lost(monkeypatch):
+    """The word set again, as by another stream's kernel, after it was read and before it is 0."""
+    from ivf_quantizer_b200 import _lib, mx4
+    a, b, queries = _index(300, 64, 12), _index(200, 64, 13), _index(3, 64, 14)
+    a.scores(queries), b.scores(queries)
+    word = mx4._words[a.codes.device.index]
+
+    class Racing:
+        def data_ptr(self):
+            return word.data_ptr()
+
+        def __int__(self):
+            code = int(word)
+            word.fill_(_lib.ERR_TIMEOUT)                # b's kernel gives up here
+            return code
+
+        def zero_(self):
+            word.zero_()
+
+    word.fill_(_lib.ERR_TIMEOUT)
+    with monkeypatch.context() as patch:
+        patch.setitem(mx4._words, a.codes.device.index, Racing())
+        assert a.status() == _lib.ERR_TIMEOUT
+    assert b.status() == _lib.ERR_TIMEOUT and b.status() == _lib.OK and a.status() == _lib.OK
