@@ -136,13 +136,16 @@ __device__ __forceinline__ uint64_t sm_weight(float x, const SmRow& r, const dou
   return (uint64_t)__double_as_longlong(m) & 0xfffffffffffffull;
 }
 
-// min-p: the least weight it keeps, and a logit that is surely below every logit of that weight.
+// min-p: the least weight it keeps, and a logit that is surely below every logit of that weight, so
+// that the comparison of weights decides alone.
 __device__ __forceinline__ uint64_t sm_min_weight(float mp) {
   return (uint64_t)__double2ull_ru((double)mp * kSmOne);
 }
-__device__ __forceinline__ float sm_min_logit(float mp, float t, const SmRow& r) {
-  // log2(mp) <= 0, a relative error of 2^-20 at most allowed for, and 2^-38 for the weights' rounding
-  const float down = fmaf(__log2f(mp), 0.6931482f * 1.00001f, -1e-5f) * t;
+__device__ __forceinline__ float sm_min_logit(uint64_t least, float t, const SmRow& r) {
+  if (least <= 1) return r.least;           // every weight that is not 0
+  // what rounds to `least` is least - 1/2 and more; the slack is 1e-5 and 2e-5 of the logarithm, against
+  // errors of 2^-24 in the argument, 2^-21 in the logarithm and 2^-23 in each product
+  const float down = fmaf(__log2f((float)(((double)least - 0.5) / kSmOne)), 0.6931482f * 1.00001f, -1e-5f) * t;
   return __double2float_rd((double)r.top + (double)down * 1.00001 - 1e-5 * (double)t);
 }
 // Bounds of a row's parameters (NaN fails them).
@@ -760,7 +763,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
       border = z.find(false, 0u, (double)p * (double)whole, from, border);
       if (border != kSmAll) from = fmaxf(from, sm_place_value(border));
     }
-    if (mp > 0.f) from = fmaxf(from, sm_min_logit(mp, t, r));
+    if (mp > 0.f) from = fmaxf(from, sm_min_logit(sm_min_weight(mp), t, r));
   }
   const uint64_t least = t > 0.f ? sm_min_weight(mp) : 0ull;   // weight that min-p asks for
   // tokens above `from` count, and those at it up to index ib
@@ -939,7 +942,7 @@ __global__ void __launch_bounds__(32 * kSmWarps) sample_warp_kernel(const SmArgs
   const SmRow r = sm_row(top, t);
   float from = r.least;
   if (t == 0.f) from = top;
-  else if (mp > 0.f) from = fmaxf(from, sm_min_logit(mp, t, r));
+  else if (mp > 0.f) from = fmaxf(from, sm_min_logit(sm_min_weight(mp), t, r));
   const uint64_t least = t > 0.f ? sm_min_weight(mp) : 0ull;   // weight that min-p asks for
   // the tokens that may be kept, in index order: most rows keep few, and their weights are then
   // computed by full warps
