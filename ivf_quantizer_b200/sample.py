@@ -2,6 +2,8 @@
 through fgmm_sample_logits (include/fgmm.h).  CUDA tensors only; argument marshalling only."""
 from __future__ import annotations
 
+import operator
+
 import torch
 
 from ._lib import LIB
@@ -17,6 +19,16 @@ def _per_row(v, name, dtype, rows, device):
         raise ValueError(f"{name} must be a number or a contiguous {dtype} [rows] tensor on the "
                          "logits' device")
     return v
+
+
+def _count(k, V):
+    """top_k as a number: an integer, and 0 .. V of it is enough to say (V and 0 keep all)."""
+    if k is None or isinstance(k, torch.Tensor):
+        return k
+    try:
+        return min(max(operator.index(k), 0), V)
+    except TypeError:
+        raise TypeError("top_k must be an integer or an int32 [rows] tensor") from None
 
 
 def sample_logits(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, top_p=None,
@@ -38,7 +50,7 @@ def sample_logits(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k
         raise ValueError("u must be a float64 [rows] tensor")
     u = _per_row(u, "u", torch.float64, rows, dev)
     temperature = _per_row(temperature, "temperature", torch.float32, rows, dev)
-    top_k = _per_row(top_k, "top_k", torch.int32, rows, dev)
+    top_k = _per_row(_count(top_k, V), "top_k", torch.int32, rows, dev)
     top_p = _per_row(top_p, "top_p", torch.float32, rows, dev)
     min_p = _per_row(min_p, "min_p", torch.float32, rows, dev)
     ids = empty(rows, None, torch.int32, dev)
