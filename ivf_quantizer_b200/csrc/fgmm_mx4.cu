@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(MxEpi<NT>::kThreads, MxCfg<NT, KB>::kCtas)
   unsigned char* outbuf = ring + C::kStages * C::kStage;
   MxBars* bars = reinterpret_cast<MxBars*>(outbuf + C::kOut);
   volatile int* abort = &bars->abort;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   const int nkc = (nb + 3) / 4;                     // scale tiles (128 dimensions) of a row
   const int nst = (nkc + C::kAtoms - 1) / C::kAtoms;  // stages of a tile
   if (threadIdx.x == 0) {
@@ -850,7 +850,7 @@ __global__ void __launch_bounds__(MxPackCfg<NT, KB>::kThreads, MxPackCfg<NT, KB>
 // overlap by 32: the epilogue drains those first, and the next tile's products wait for them alone.
 template <typename T>
 struct MxPairCfg {
-  static constexpr int NT = 256, KB = 128, kAtoms = 2;
+  static constexpr int NT = 256, KB = 128;
   static constexpr int kA = kMxBM * KB, kB = NT / 2 * KB, kSf = 1024;
   static constexpr int kStage = kA + kB + 3 * kSf;  // own vectors, half of the queries; scales: own, all
   static constexpr int kGroups = 4, kWarps = 4 * kGroups, kThreads = 128 + 32 * kWarps;
@@ -1233,10 +1233,10 @@ cudaError_t mx_encode(const T* X, int64_t n, int D, int64_t ldx, int nb, int nkc
   const int64_t most = (int64_t)sms * (tiles ? 32 : 16);
   const unsigned grid = (unsigned)(blocks < most ? blocks : most);
   auto* k = tiles ? (rows_at(32) ? mx4_encode_kernel<T, 32, true> : mx4_encode_kernel<T, 16, true>)
-            : rows_at(16)                  ? mx4_encode_kernel<T, 16, false>
-            : rows_at(8)                   ? mx4_encode_kernel<T, 8, false>
-            : sizeof(T) == 4 || rows_at(4) ? mx4_encode_kernel<T, 4, false>
-                                           : mx4_encode_kernel<T, 2, false>;
+            : rows_at(16) ? mx4_encode_kernel<T, 16, false>
+            : rows_at(8)  ? mx4_encode_kernel<T, 8, false>
+            : rows_at(4)  ? mx4_encode_kernel<T, 4, false>
+                          : mx4_encode_kernel<T, (int)sizeof(T), false>;
   k<<<grid, kMxThreads, 0, s>>>(X, n, D, ldx, nb, nkc, codes, scales);
   return cudaGetLastError();
 }
@@ -1257,8 +1257,10 @@ cudaError_t mx_decode(const uint8_t* codes, const uint8_t* scales, int64_t n, in
   if (rows_at(32)) return mx_decode_by<T, 32, 32>(codes, scales, n, D, out, ldo, s);
   if (rows_at(16)) return mx_decode_by<T, 16, 16>(codes, scales, n, D, out, ldo, s);
   if (rows_at(8)) return mx_decode_by<T, 16, 8>(codes, scales, n, D, out, ldo, s);
-  if (sizeof(T) == 4 || rows_at(4)) return mx_decode_by<T, 16, 4>(codes, scales, n, D, out, ldo, s);
-  return mx_decode_by<T, 8, 2>(codes, scales, n, D, out, ldo, s);
+  if constexpr (sizeof(T) == 2) {
+    if (!rows_at(4)) return mx_decode_by<T, 8, 2>(codes, scales, n, D, out, ldo, s);
+  }
+  return mx_decode_by<T, 16, 4>(codes, scales, n, D, out, ldo, s);
 }
 
 }  // namespace
