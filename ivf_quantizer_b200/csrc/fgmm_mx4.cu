@@ -10,7 +10,7 @@
 #include <type_traits>
 
 #include "fgmm_internal.h"
-#include "sm100_ptx.cuh"
+#include "mxf4_ptx.cuh"
 
 namespace fgmm {
 namespace {

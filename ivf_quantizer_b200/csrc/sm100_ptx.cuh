@@ -31,11 +31,6 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
 
-// Programmatic dependent launch: the kernel before lets the next one start its prologue; that one
-// waits, before its first access to memory, until the kernels before have ended.
-__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // ------------------------------------------------------------------ mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count)
@@ -86,82 +81,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
-// mbar_wait that leaves the thread suspended for up to 20 us a try, so that waiting warps do not take
-// issue slots and shared-memory cycles from the thread that feeds the tensor cores, and that looks at
-// the (slow) global timer between tries only.
-__device__ __forceinline__ bool mbar_try_wait_long(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait_soon(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  for (int i = 0; i < 64; ++i)
-    if (mbar_try_wait_long(bar, parity)) return true;
-  return mbar_wait(bar, parity, abort);
-}
-// The same by every lane of a warp, which then goes on or gives up as a whole.
-__device__ __forceinline__ bool mbar_wait_all(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xffffffffu, mbar_wait_soon(bar, parity, abort));
-}
-// One lane of a converged warp.  Roles that issue copies or products run as whole warps and issue
-// under this: their operands then are uniform values, which the instructions want.  Issued by code
-// that one lane runs alone, each tcgen05 instruction took about 95 cycles.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r != 0;
-}
-__device__ __forceinline__ bool mbar_wait_warp_soon(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  int ok = 1;
-  if ((threadIdx.x & 31u) == 0) ok = mbar_wait_soon(bar, parity, abort) ? 1 : 0;
-  ok = __shfl_sync(0xffffffffu, ok, 0);
-  __syncwarp();
-  return ok != 0;
-}
-
-// Arrive on the mbarrier at this address in CTA `rank` of the cluster.
-__device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t rank) {
-  asm volatile(
-      "{\n\t.reg .b32 ra;\n\tmapa.shared::cluster.u32 ra, %0, %1;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [ra];\n\t}" ::"r"(smem_u32(bar)),
-      "r"(rank)
-      : "memory");
-}
-// mbar_wait for a barrier that another CTA of the cluster arrives on.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 1;; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
-        : "memory");
-    if (ok) return true;
-    if ((i & 63u) == 0) {
-      if (abort && *abort) return false;
-      const uint64_t now = globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > kWaitLimitNs) return false;
-    }
-  }
-}
-__device__ __forceinline__ bool mbar_wait_cluster_all(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, abort));
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-
 // Bounded wait of a whole warp: lane 0 alone polls the mbarrier (barrier operations of
 // 32 lanes on one word are serialised by the shared-memory pipe, which the tensor cores'
 // operand reads and the TMA share), then the warp synchronises with it; the warp's other
@@ -191,30 +110,6 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const void* tmap, ui
       : "memory");
 }
 
-// Loads of a CTA pair (cta_group::2): into this CTA's shared memory, counted on the mbarrier with the
-// shared::cluster address `bar`, which may be the other CTA's (cluster_addr).
-__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const void* tmap, uint32_t bar, int x,
-                                                 int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(smem_dst)),
-      "l"(tmap), "r"(bar), "r"(x), "r"(y)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const void* tmap, uint32_t bar, int x,
-                                                 int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
-      "l"(tmap), "r"(bar), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
 // Untiled bulk copy global -> shared (16-byte aligned addresses, size a multiple of 16).
 __device__ __forceinline__ void bulk_load(void* smem_dst, const void* gsrc, uint32_t bytes,
                                           uint64_t* bar) {
@@ -223,22 +118,6 @@ __device__ __forceinline__ void bulk_load(void* smem_dst, const void* gsrc, uint
           "r"(smem_u32(smem_dst)),
       "l"(gsrc), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
-}
-
-// Untiled bulk copy shared -> global (16-byte aligned addresses, size a multiple of 16), in the
-// thread's current bulk group.
-__device__ __forceinline__ void bulk_store(void* gdst, uint32_t ssrc, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(gdst), "r"(ssrc),
-               "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_commit() {
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-// Until at most N of the thread's bulk groups still read their shared memory.
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
 // Bulk prefetch of global memory into L2 (16-byte aligned address, size a multiple of 16).
@@ -297,64 +176,6 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-
-// D[tmem] (+)= A[smem desc] x B[smem desc], kind::mxf4: e2m1 operands, K = 64 a product, one
-// e8m0 scale per 32 of K for every row of A and of B in tensor memory (two of them a product).
-__device__ __forceinline__ void mma_mxf4_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
-                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], "
-      "p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
-      : "memory");
-}
-
-// Copy 512 bytes of shared memory (32 rows of 16 bytes) to four TMEM columns: row l to lane l of
-// every warp's lane quarter.  Executes in order with the tcgen05.mma of the same thread.
-__device__ __forceinline__ void tmem_cp_32x128(uint32_t taddr, uint64_t s_desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc)
-               : "memory");
-}
-
-// The same for a pair of CTAs (cta_group::2): 256 rows of A, 128 in each CTA's shared memory, B's rows
-// split likewise; every CTA's accumulator holds its 128 rows.  Descriptors hold for both CTAs.
-__device__ __forceinline__ void mma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                              uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
-                                              uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], "
-      "p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_cp_32x128_pair(uint32_t taddr, uint64_t s_desc) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc)
-               : "memory");
-}
-// Arrive on the mbarrier at this address in both CTAs of the pair once the products complete.
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], "
-      "%1;" ::"r"(smem_u32(bar)),
-      "h"((uint16_t)3)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                   smem_u32(dst_smem)),
-               "r"(ncols)
-               : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish_pair() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
-               : "memory");
 }
 
 // Arrive on an mbarrier once every previously issued tcgen05.mma of this thread completes.
@@ -444,29 +265,6 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint64_t hi) {
   return hi | (uint64_t)((saddr >> 4) & 0x3FFFu);
 }
 
-// The same for 64-byte-swizzled tiles (rows of 64 bytes, 8-row atoms of 512).
-__host__ __device__ constexpr uint64_t sw64_hi(uint32_t lbo_bytes, uint32_t sbo_bytes) {
-  return ((uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((sbo_bytes >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) |
-         ((uint64_t)4 << 61);
-}
-
-// Barrier of `threads` threads of the CTA (whole warps), id 1 .. 15.
-__device__ __forceinline__ void named_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-// The same, telling every thread whether `ok` held on all of them.
-__device__ __forceinline__ bool named_all(int id, int threads, bool ok) {
-  int r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %3, 0;\n\tbar.red.and.pred q, %1, %2, p;\n\t"
-      "selp.b32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(threads), "r"((int)ok)
-      : "memory");
-  return r != 0;
-}
-
 // ------------------------------------------------------------------ packed fp32 and exp2
 // Two fp32 lanes in one 64-bit register (sm_100 f32x2 arithmetic, round to nearest).
 __device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
@@ -501,21 +299,6 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn_major, 
          | (0u << 7) | (0u << 10)        // A, B format f16
          | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-// kind::mxf4 instruction descriptor: A, B e2m1 K-major, scales e8m0; sf selects which two of the
-// four scale bytes of a TMEM word apply (0: the lower, 2: the upper two), for A and B alike.
-//   [4,6) B scale id | [7,10) A fmt (1 = e2m1) | [10,12) B fmt | [17,23) N>>3 | [23] e8m0 |
-//   [27,29) M>>7 | [29,31) A scale id
-__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, uint32_t sf) {
-  return (sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
-         ((uint32_t)(M >> 7) << 27) | (sf << 29);
-}
-
-// Descriptor of an unswizzled matrix of 16-byte rows, 8-row groups of 128 contiguous bytes.
-__device__ __forceinline__ uint64_t rows16_desc(uint32_t saddr) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)8 << 16) | ((uint64_t)8 << 32) |
-         ((uint64_t)1 << 46);
 }
 
 }  // namespace ptx
