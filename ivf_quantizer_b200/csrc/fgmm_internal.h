@@ -263,6 +263,13 @@ cudaError_t launch_ivf_search(int K, int D, const float* C, const int64_t* offse
                               const int64_t* entries, const float* X, int64_t ldx, const float* Q,
                               int64_t nq, int64_t ldq, int nprobe, int topk, int64_t* out_i,
                               float* out_d, int64_t* dco, cudaStream_t s);
+// The driver's tensor-map encoder, fetched through the runtime so that the library does not link
+// libcuda (it must load on hosts without a driver); NULL when there is none (fgmm_tc.cu).
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled();
 // 4-bit codes (fgmm_mx4.cu)
 cudaError_t launch_mx4_encode(const void* X, int x_dtype, int64_t n, int D, int64_t ldx,
                               uint8_t* codes, uint8_t* scales, cudaStream_t s);

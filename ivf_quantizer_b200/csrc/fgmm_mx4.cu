@@ -1067,27 +1067,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxPairCfg<T>::kThrea
   }
 }
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn mx_encode_tiled() {
-  static EncodeTiledFn fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    return cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-                       cudaSuccess && q == cudaDriverEntryPointSuccess
-               ? reinterpret_cast<EncodeTiledFn>(p) : nullptr;
-  }();
-  return fn;
-}
-
 // Rows of codes as boxes of `box_bytes` (64 or 128, swizzled as wide) x `box_rows`; what lies beyond
 // a row or the last row is 0.
 bool mx_tmap(CUtensorMap* map, const uint8_t* codes, int nb, int64_t rows, int box_bytes,
              int box_rows) {
-  EncodeTiledFn enc = mx_encode_tiled();
+  EncodeTiledFn enc = encode_tiled();
   if (!enc) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)nb * 16, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)nb * 16};
@@ -1101,7 +1085,7 @@ bool mx_tmap(CUtensorMap* map, const uint8_t* codes, int nb, int64_t rows, int b
 
 // Scale tiles [rows of tiles][tiles of a row][512 bytes] as boxes of 2 of a row x `box_rows`.
 bool mx_tmap_scales(CUtensorMap* map, const uint8_t* scales, int nb, int64_t rows, int box_rows) {
-  EncodeTiledFn enc = mx_encode_tiled();
+  EncodeTiledFn enc = encode_tiled();
   if (!enc) return false;
   const cuuint64_t nkc = (cuuint64_t)(nb + 3) / 4;
   const cuuint64_t dims[3] = {128, nkc, (cuuint64_t)(rows + 127) / 128};

@@ -52,6 +52,8 @@
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
+#include <atomic>
+
 #include "fgmm_internal.h"
 #include "sm100_ptx.cuh"
 
@@ -1135,27 +1137,21 @@ cudaError_t run_bounded_wait_probe(int64_t limit_ns, int* status_host) {
 }
 
 // ------------------------------------------------------------------ host side
-namespace {
-
-// The driver's tensor-map encoder, fetched through the runtime so that the library
-// does not link libcuda (it must load on hosts without a driver).
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 EncodeTiledFn encode_tiled() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
+  static std::atomic<EncodeTiledFn> fn{nullptr};   // (stateless calls come from any thread)
+  EncodeTiledFn got = fn.load();
+  if (!got) {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
             cudaSuccess &&
         q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
+      fn.store(got = reinterpret_cast<EncodeTiledFn>(p));
   }
-  return fn;
+  return got;
 }
+
+namespace {
 
 bool make_tmap(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t rows) {
   EncodeTiledFn enc = encode_tiled();
