@@ -881,6 +881,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
 // One warp a row, for rows of at most kSmWarpV values without top-k and top-p: a CTA a row spends
 // its time on barriers there.  The row lies in shared memory, and loops are short: with the row in
 // registers and every loop unrolled, the warps waited for instructions.
+//
+// us, a CTA and a warp a row, fp32, no cut / with min-p: 16384 rows x 128 69 / 72 and 24 / 20, x 1024 87 / 84
+// and 73 / 35, x 1500 126 / 118 and 125 / 59, x 2000 144 / 129 and 286 / 76; 4096 x 1024 25 / 24 and 22 / 11.
+// With min-p a warp is faster beyond 1024 as well, without a cut it is not, and a single row of 1024 without a
+// cut takes it 9.9 against 5.1 (one of 256 5.4 and 4.9, of 128 4.1 and 4.7): one lane weighs 32 tokens.
 constexpr int kSmWarpV = 1024, kSmWarps = 4;
 
 template <typename T>
@@ -1037,8 +1042,11 @@ cudaError_t sm_choose(SmArgs a, int64_t rows, cudaStream_t st) {
     a.slice = a.V;
     return sm_launch<T, kSmall, true>(a, rows, 1, kFixedSmall + bytes(1), st);
   }
-  // CTAs a row: while the rows leave SMs idle, and until a slice has at most 32768 tokens (a row of
-  // 131072 by one CTA 228 us, by two 208, by four 199, by eight 244, at 256 rows)
+  // CTAs a row: while the rows leave SMs idle, and until a slice has at most 32768 tokens.  us with slices of
+  // at most 16384 / 32768 / 65536 / 131072, top-p: fp32 256 x 50021 117 / 73 / 87 / 87, 256 x 131072 274 / 162 /
+  // 174 / 249, 300 x 70000 214 / 155 / 117 / 120, 256 x 262144 (eight CTAs at most) - / 316 / 323 / 352; bf16
+  // 256 x 131072 257 / 200 / 175 / 194, 1024 x 50021 378 / 278 / 251 / 250.  Fastest in fp32 but for rows just
+  // above a power of two of slices; half as many tokens' bytes in bf16 would bear 65536
   int C = 1;
   while (C < 8 && (a.V / C > 32768 || (rows * C < sms && a.V / C > 4096))) C *= 2;
   a.slice = (a.V + C - 1) / C;
