@@ -438,7 +438,8 @@ int fgmm_ivf_search(int K, int D, const float* centroids, const int64_t* offsets
  * alignment of its elements' own size.
  *
  * fgmm_mx4_decode: the values that the codes stand for, exactly, as FGMM_F32 or FGMM_BF16 rows
- * of stride ldo.
+ * of stride ldo (scale bytes 253 and 254, which encoding never makes, reach beyond the largest
+ * finite value: infinity).
  *
  * fgmm_mx4_scores: out[m][n] = alpha * sum_d q[m][d] x[n][d] + bias[n] for codes of M queries and
  * of N vectors of the same D (the padding adds 0); bias: optional device float[N] (-|x|^2 / 2

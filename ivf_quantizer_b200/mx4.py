@@ -115,7 +115,8 @@ class MX4:
         return self.codes.numel() + self.scales.numel()
 
     def decode(self, dtype: torch.dtype = torch.float32) -> torch.Tensor:
-        """The rows that the codes stand for, [N, D], float32 or bfloat16 (exact in both)."""
+        """The rows that the codes stand for, [N, D], float32 or bfloat16 (exact in both; infinity where
+        a scale of 2^126 or 2^127, which encoding never makes, takes a code beyond them)."""
         if dtype not in _DTYPES:
             raise TypeError("dtype must be float32 or bfloat16")
         N, D = self.shape
