@@ -36,7 +36,8 @@ def sample_logits(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k
     """Draws one index per row of logits [rows, V] (float32 or bfloat16; -inf forbids an index).
 
     u: float64 [rows] uniforms in [0, 1).  temperature, top_p, min_p (float32) and top_k (int32):
-    a number for all rows, a [rows] tensor, or None for no effect.  Truncation in the order top-k,
+    a number for all rows, a [rows] tensor (which saves the launch that fills one with the number),
+    or None for no effect.  Truncation in the order top-k,
     top-p (of the weight that top-k left), min-p (relative to the largest weight); temperature 0
     takes the first maximum.
 
