@@ -143,8 +143,8 @@ __device__ __forceinline__ uint64_t sm_min_weight(float mp) {
 }
 __device__ __forceinline__ float sm_min_logit(uint64_t least, float t, const SmRow& r) {
   if (least <= 1) return r.least;           // every weight that is not 0
-  // what rounds to `least` is least - 1/2 and more; the slack is 1e-5 and 2e-5 of the logarithm, against
-  // errors of 2^-24 in the argument, 2^-21 in the logarithm and 2^-23 in each product
+  // what rounds to `least` is least - 1/2 and more; the slack, 1e-5 and 2e-5 of the logarithm (at most 28),
+  // covers the rounding of the argument (6e-8), two ulps of __log2f (2^-22 near 1, 5e-6 at 41) and the products'
   const float down = fmaf(__log2f((float)(((double)least - 0.5) / kSmOne)), 0.6931482f * 1.00001f, -1e-5f) * t;
   return __double2float_rd((double)r.top + (double)down * 1.00001 - 1e-5 * (double)t);
 }
