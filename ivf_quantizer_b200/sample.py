@@ -22,13 +22,14 @@ def _per_row(v, name, dtype, rows, device):
 
 
 def _count(k, V):
-    """top_k as a number: an integer, and 0 .. V of it is enough to say (V and 0 keep all)."""
+    """top_k as a number: a whole one, of which 0 .. V is enough to say (V and 0 keep all)."""
     if k is None or isinstance(k, torch.Tensor):
         return k
     try:
-        return min(max(operator.index(k), 0), V)
+        k = int(k) if isinstance(k, float) and k.is_integer() else operator.index(k)
     except TypeError:
-        raise TypeError("top_k must be an integer or an int32 [rows] tensor") from None
+        raise TypeError("top_k must be a whole number or an int32 [rows] tensor") from None
+    return min(max(k, 0), V)
 
 
 def sample_logits(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, top_p=None,

@@ -8,8 +8,9 @@ def test_top_k_as_a_number_is_an_integer_of_any_size():
     from ivf_quantizer_b200.sample import _count
     t = torch.zeros(3, dtype=torch.int32)
     assert _count(None, 50) is None and _count(t, 50) is t
-    assert [_count(k, 50) for k in (0, 1, 50, 51, 1 << 40, -1, -(1 << 40), np.int64(7))] == [0, 1, 50, 50, 50, 0, 0, 7]
-    for bad in (2.5, 3.0, "3", float("nan")):
+    assert [_count(k, 50) for k in (0, 1, 50, 51, 1 << 40, -1, -(1 << 40), np.int64(7), 7.0, 1e30)] == \
+        [0, 1, 50, 50, 50, 0, 0, 7, 7, 50]
+    for bad in (2.5, "3", float("nan"), float("inf")):
         with pytest.raises(TypeError):
             _count(bad, 50)
 
